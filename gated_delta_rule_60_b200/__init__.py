@@ -12,5 +12,9 @@ from .binding import (KdaError, kda_chunk_bwd, kda_chunk_bwd_workspace_size,  # 
                       kda_chunk_fwd_softplus, kda_chunk_fwd_workspace_size,
                       kda_debug_range_prefill, kda_debug_range_read,
                       kda_debug_stall_prefill, kda_decode_step, kda_decode_step_softplus,
-                      kda_prologue, kda_selftest_wait_timeout, kda_status_string,
+                      kda_layernorm_bwd, kda_layernorm_bwd_workspace_size, kda_layernorm_fwd,
+                      kda_linear_chunk_bwd, kda_linear_chunk_bwd_workspace_size,
+                      kda_linear_chunk_fwd, kda_linear_chunk_fwd_workspace_size,
+                      kda_linear_decode_step, kda_prologue, kda_rotary,
+                      kda_rotary_frequencies, kda_selftest_wait_timeout, kda_status_string,
                       kda_stream_status, kda_version, load_library)

@@ -11,6 +11,7 @@ The Python names are the C names.  As in the C ABI, the tensors of a call
 must live on the current CUDA device (select it with torch.cuda.set_device or
 a torch.cuda.device context); stream=None means that device's current stream.
 """
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -96,6 +97,36 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kda_debug_range_prefill.argtypes = [i32]
     lib.kda_debug_range_read.restype = ctypes.c_int
     lib.kda_debug_range_read.argtypes = [ctypes.POINTER(ctypes.c_float), sz]
+    lib.kda_linear_chunk_fwd_workspace_size.restype = sz
+    lib.kda_linear_chunk_fwd_workspace_size.argtypes = [i32, i64, i32, i32, ctypes.c_int]
+    lib.kda_linear_chunk_fwd.restype = ctypes.c_int
+    lib.kda_linear_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32,
+                                         ctypes.c_int, i32, ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.kda_linear_decode_step.restype = ctypes.c_int
+    lib.kda_linear_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                           ctypes.c_int, i32, ctypes.c_float, vp]
+    lib.kda_linear_chunk_bwd_workspace_size.restype = sz
+    lib.kda_linear_chunk_bwd_workspace_size.argtypes = [i32, i64, i32, i32, i32, ctypes.c_int]
+    lib.kda_linear_chunk_bwd.restype = ctypes.c_int
+    lib.kda_linear_chunk_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32,
+                                         ctypes.c_int, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp,
+                                         vp, vp, sz, vp]
+    lib.kda_rotary.restype = ctypes.c_int
+    lib.kda_rotary.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, ctypes.c_int, i32,
+                               i32, ctypes.c_float, i64, i64, vp, vp, i64, i64, vp]
+    lib.kda_rotary_frequencies.restype = ctypes.c_int
+    lib.kda_rotary_frequencies.argtypes = [i32, ctypes.c_double, ctypes.c_int, ctypes.c_double,
+                                           ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                           ctypes.POINTER(ctypes.c_float),
+                                           ctypes.POINTER(ctypes.c_float)]
+    lib.kda_layernorm_fwd.restype = ctypes.c_int
+    lib.kda_layernorm_fwd.argtypes = [vp, vp, vp, i64, i32, i32, ctypes.c_int, ctypes.c_float, vp,
+                                      vp, vp, vp]
+    lib.kda_layernorm_bwd_workspace_size.restype = sz
+    lib.kda_layernorm_bwd_workspace_size.argtypes = [i64, i32, i32, ctypes.c_int]
+    lib.kda_layernorm_bwd.restype = ctypes.c_int
+    lib.kda_layernorm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i32, i32, ctypes.c_int, vp, vp, vp,
+                                      vp, sz, vp]
     _lib = lib
     return lib
 
@@ -481,6 +512,367 @@ def kda_debug_range_read() -> dict:
     n = len(RANGE_COLS)
     return {r: {c: float(buf[i * n + j]) for j, c in enumerate(RANGE_COLS)}
             for i, r in enumerate(RANGE_ROWS)}
+
+
+def _current(t: torch.Tensor, name: str):
+    """The device of t, which has to be the current CUDA device (the launch
+    goes there whatever the tensors say)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("%s must be on cuda, got %s" % (name, dev))
+    if dev.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, which is not the current device" % (name, dev))
+    return dev
+
+
+def _on(stream):
+    """Where a call allocates: torch's memory belongs to a stream, so what a
+    call on another stream writes has to come from that stream's."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _workspace(need: int, given: Optional[torch.Tensor], dev):
+    """(pointer, bytes, tensor) of a call's scratch: the caller's, or a new one."""
+    if given is None:
+        if not need:
+            return None, 0, None
+        given = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif given.device != dev or not given.is_contiguous():
+        raise ValueError("workspace must be contiguous on %s" % dev)
+    return _ptr(given), given.numel() * given.element_size(), given
+
+
+def _linear_sizes(q, v, g, cu_seqlens, num_seqs):
+    """(device, T, Hk, H, d, dtype, N, g_per_token) of a linear-attention call."""
+    dev = _current(q, "q")
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("q, k and v must have three dimensions")
+    T, Hk, d = q.shape
+    H = v.shape[1]
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise TypeError("unsupported dtype %s" % dt)
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
+        N = cu_seqlens.numel() - 1
+    else:
+        N = 1 if num_seqs is None else int(num_seqs)
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    per_token = g.dim() == 2
+    _check(g, "g", torch.float32, (T, H) if per_token else (H,), dev)
+    return dev, T, Hk, H, d, dt, N, int(per_token)
+
+
+def kda_linear_chunk_fwd_workspace_size(N: int, T_tot: int, H: int, d: int,
+                                        dtype: torch.dtype) -> int:
+    return int(load_library().kda_linear_chunk_fwd_workspace_size(int(N), int(T_tot), int(H),
+                                                                  int(d), _DTYPES[dtype]))
+
+
+def kda_linear_chunk_bwd_workspace_size(N: int, T_tot: int, Hk: int, H: int, d: int,
+                                        dtype: torch.dtype) -> int:
+    return int(load_library().kda_linear_chunk_bwd_workspace_size(
+        int(N), int(T_tot), int(Hk), int(H), int(d), _DTYPES[dtype]))
+
+
+def kda_linear_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                         h0: Optional[torch.Tensor] = None,
+                         cu_seqlens: Optional[torch.Tensor] = None, *,
+                         num_seqs: Optional[int] = None, scale: float = 1.0,
+                         o: Optional[torch.Tensor] = None, hT: Optional[torch.Tensor] = None,
+                         output_final_state: bool = True,
+                         workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head over packed sequences:
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  Returns
+    (o [T, H, d], hT [N, H, d, d] fp32 or None).
+
+    q, k [T, Hk, d] and v [T, H, d] share one dtype (bf16 or fp32), H a
+    multiple of Hk; g fp32 log-decays, [T, H] or one constant a head [H]; h0
+    fp32 [N, H, d, d] or None; hT may be h0; cu_seqlens int32 [N + 1], or None
+    with num_seqs sequences of equal length.
+    """
+    lib = load_library()
+    dev, T, Hk, H, d, dt, N, per_token = _linear_sizes(q, v, g, cu_seqlens, num_seqs)
+    _check(q, "q", dt, (T, Hk, d), dev)
+    _check(k, "k", dt, (T, Hk, d), dev)
+    _check(v, "v", dt, (T, H, d), dev)
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, (N, H, d, d), dev)
+    if o is not None:
+        _check(o, "o", dt, (T, H, d), dev)
+    if hT is not None:
+        _check(hT, "hT", torch.float32, (N, H, d, d), dev)
+    need = lib.kda_linear_chunk_fwd_workspace_size(N, T, H, d, _DTYPES[dt])
+    with _on(stream):
+        if o is None:
+            o = torch.empty(T, H, d, dtype=dt, device=dev)
+        if hT is None and output_final_state:
+            hT = torch.empty(N, H, d, d, dtype=torch.float32, device=dev)
+        ws, ws_bytes, _keep = _workspace(need, workspace, dev)
+    st = lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(cu_seqlens),
+                                  N, T, Hk, H, d, _DTYPES[dt], per_token, float(scale), _ptr(o),
+                                  _ptr(hT), ws, ws_bytes, _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_chunk_fwd")
+    return o, hT
+
+
+def kda_linear_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                           S: torch.Tensor, *, scale: float = 1.0,
+                           o: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of the linear attention for each sequence; S [B, H, d, d]
+    fp32 is updated in place.  q, k [B, Hk, d], v [B, H, d], g fp32 [B, H] or
+    [H].  Returns o [B, H, d]."""
+    lib = load_library()
+    dev, B, Hk, H, d, dt, _, per_token = _linear_sizes(q, v, g, None, 1)
+    _check(q, "q", dt, (B, Hk, d), dev)
+    _check(k, "k", dt, (B, Hk, d), dev)
+    _check(v, "v", dt, (B, H, d), dev)
+    _check(S, "S", torch.float32, (B, H, d, d), dev)
+    if o is not None:
+        _check(o, "o", dt, (B, H, d), dev)
+    else:
+        with _on(stream):
+            o = torch.empty(B, H, d, dtype=dt, device=dev)
+    st = lib.kda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(o), B, Hk, H,
+                                    d, _DTYPES[dt], per_token, float(scale),
+                                    _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_decode_step")
+    return o
+
+
+def kda_linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                         dO: torch.Tensor, h0: Optional[torch.Tensor] = None,
+                         cu_seqlens: Optional[torch.Tensor] = None,
+                         dhT: Optional[torch.Tensor] = None, *, num_seqs: Optional[int] = None,
+                         scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> dict:
+    """Gradient of kda_linear_chunk_fwd for L = <dO, o> + <dhT, hT>: a dict of
+    dq, dk [T, Hk, d], dv [T, H, d] (dtype of q), dg fp32 of g's shape and
+    dh0 [N, H, d, d] fp32."""
+    lib = load_library()
+    dev, T, Hk, H, d, dt, N, per_token = _linear_sizes(q, v, g, cu_seqlens, num_seqs)
+    _check(q, "q", dt, (T, Hk, d), dev)
+    _check(k, "k", dt, (T, Hk, d), dev)
+    _check(v, "v", dt, (T, H, d), dev)
+    _check(dO, "dO", dt, (T, H, d), dev)
+    for t, name in ((h0, "h0"), (dhT, "dhT")):
+        if t is not None:
+            _check(t, name, torch.float32, (N, H, d, d), dev)
+    need = lib.kda_linear_chunk_bwd_workspace_size(N, T, Hk, H, d, _DTYPES[dt])
+    with _on(stream):
+        out = {"dq": torch.empty(T, Hk, d, dtype=dt, device=dev),
+               "dk": torch.empty(T, Hk, d, dtype=dt, device=dev),
+               "dv": torch.empty(T, H, d, dtype=dt, device=dev),
+               "dg": torch.empty(g.shape, dtype=torch.float32, device=dev),
+               "dh0": torch.empty(N, H, d, d, dtype=torch.float32, device=dev)}
+        ws, ws_bytes, _keep = _workspace(need, workspace, dev)
+    st = lib.kda_linear_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(cu_seqlens),
+                                  N, T, Hk, H, d, _DTYPES[dt], per_token, float(scale), _ptr(dO),
+                                  _ptr(dhT), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+                                  _ptr(out["dg"]), _ptr(out["dh0"]), ws, ws_bytes,
+                                  _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_chunk_bwd")
+    return out
+
+
+KDA_ROPE_NONE = 0
+KDA_ROPE_LINEAR = 1
+KDA_ROPE_BASE = 2
+KDA_ROPE_PARTS = 3
+
+
+def kda_rotary_frequencies(rot: int, base: float = 10000.0, scaling: int = KDA_ROPE_NONE,
+                           factor: float = 1.0, original_length: float = 0.0,
+                           beta_fast: float = 32.0, beta_slow: float = 1.0, *,
+                           device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq fp32 [rot / 2], scale) for kda_rotary; see include/kda.h for
+    the ways of scaling.  inv_freq is on `device` (default: the current CUDA
+    device)."""
+    rot = int(rot)
+    buf = (ctypes.c_float * max(1, rot // 2))()
+    scale = ctypes.c_float()
+    st = load_library().kda_rotary_frequencies(rot, float(base), int(scaling), float(factor),
+                                               float(original_length), float(beta_fast),
+                                               float(beta_slow), buf, ctypes.byref(scale))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rotary_frequencies")
+    inv = torch.tensor(list(buf), dtype=torch.float32)
+    return inv.to("cuda" if device is None else device), float(scale.value)
+
+
+def _token_rows(t: torch.Tensor, name: str, dt, T: int, d: int, dev) -> int:
+    """Elements between the tokens of a [T, heads, d] tensor whose token rows
+    are dense (the tokens themselves may be apart: a slice of a projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != dev:
+        raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+    if t.dtype != dt:
+        raise TypeError("%s must be %s, got %s" % (name, dt, t.dtype))
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise ValueError("%s must have shape (%d, heads, %d), got %s" % (name, T, d,
+                                                                         tuple(t.shape)))
+    s, heads = t.stride(), t.shape[1]
+    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d) or (T > 1 and s[0] < heads * d):
+        raise ValueError("%s must have dense heads, got strides %s" % (name, s))
+    return s[0] if T > 1 else heads * d
+
+
+def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+               positions: Optional[torch.Tensor] = None,
+               cu_seqlens: Optional[torch.Tensor] = None, *, num_seqs: Optional[int] = None,
+               interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
+               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary positions of q [T, Hq, d] and k [T, Hk, d] (or None) over the
+    first 2 * len(inv_freq) channels of each head.  Returns (q_out, k_out);
+    in place with q_out=q, k_out=k.
+
+    Tokens may be apart (a slice of a fused projection); heads are dense.
+    positions int32 [T], or None: a token's index in its sequence by
+    cu_seqlens / num_seqs.  inverse turns back, which is also the gradient.
+    """
+    lib = load_library()
+    dev = _current(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must have three dimensions")
+    T, Hq, d = q.shape
+    dt = q.dtype
+    if dt not in _DTYPES:
+        raise TypeError("unsupported dtype %s" % dt)
+    sq = _token_rows(q, "q", dt, T, d, dev)
+    rot = 0
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
+        rot = 2 * inv_freq.numel()
+    if positions is not None:
+        _check(positions, "positions", torch.int32, (T,), dev)
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
+        N = cu_seqlens.numel() - 1
+    else:
+        N = 1 if num_seqs is None else int(num_seqs)
+    if q_out is None:
+        with _on(stream):
+            q_out = torch.empty(T, Hq, d, dtype=dt, device=dev)
+    elif tuple(q_out.shape) != (T, Hq, d):
+        raise ValueError("q_out must have shape %s" % ((T, Hq, d),))
+    Hk = sk = sko = 0
+    if k is not None:
+        sk = _token_rows(k, "k", dt, T, d, dev)
+        Hk = k.shape[1]
+        if k_out is None:
+            with _on(stream):
+                k_out = torch.empty(T, Hk, d, dtype=dt, device=dev)
+        elif tuple(k_out.shape) != (T, Hk, d):
+            raise ValueError("k_out must have shape %s" % ((T, Hk, d),))
+        sko = _token_rows(k_out, "k_out", dt, T, d, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    st = lib.kda_rotary(_ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(cu_seqlens), N, T,
+                        Hq, Hk, d, rot, _DTYPES[dt], int(bool(interleaved)), int(bool(inverse)),
+                        float(scale), sq, sk, _ptr(q_out), _ptr(k_out),
+                        _token_rows(q_out, "q_out", dt, T, d, dev), sko, _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_rotary")
+    return q_out, k_out
+
+
+def _norm_sizes(x, weight):
+    """(device, T, G, D, dtype): weight [D] norms the last axis, [G, D] the
+    last axis of x [..., G, D] with a row for each of G."""
+    dev = _current(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have a last axis")
+    dt = x.dtype
+    if dt not in _DTYPES:
+        raise TypeError("unsupported dtype %s" % dt)
+    D = x.shape[-1]
+    G = 1
+    if weight is not None and weight.dim() == 2:
+        G = weight.shape[0]
+        if x.dim() < 2 or x.shape[-2] != G:
+            raise ValueError("a weight of shape %s needs x of shape (..., %d, %d)" % (
+                tuple(weight.shape), G, D))
+    if D == 0 or G == 0:
+        raise ValueError("x must have a last axis")
+    _check(x, "x", dt, x.shape, dev)
+    return dev, x.numel() // (G * D), G, D, dt
+
+
+def kda_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                      bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                      y: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm over the last axis of x: (y, mean, rstd), mean and rstd fp32
+    of x's shape without that axis.  weight, bias fp32 [D], or [G, D] with a
+    row for each of the G in x [..., G, D] (heads); y may be x."""
+    lib = load_library()
+    dev, T, G, D, dt = _norm_sizes(x, weight if weight is not None else bias)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _check(t, name, torch.float32, (G, D) if t.dim() == 2 else (D,), dev)
+            if t.numel() != G * D:
+                raise ValueError("weight and bias must have one shape")
+    if y is not None:
+        _check(y, "y", dt, x.shape, dev)
+    with _on(stream):
+        if y is None:
+            y = torch.empty_like(x)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    st = lib.kda_layernorm_fwd(_ptr(x), _ptr(weight), _ptr(bias), T, G, D, _DTYPES[dt], float(eps),
+                               _ptr(y), _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_layernorm_fwd")
+    return y, mean, rstd
+
+
+def kda_layernorm_bwd_workspace_size(T: int, G: int, D: int, dtype: torch.dtype) -> int:
+    return int(load_library().kda_layernorm_bwd_workspace_size(int(T), int(G), int(D),
+                                                               _DTYPES[dtype]))
+
+
+def kda_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                      weight: Optional[torch.Tensor] = None, *, bias: bool = False,
+                      dx: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradient of kda_layernorm_fwd: a dict of dx (dtype of x), dweight (with
+    a weight) and dbias (with bias=True), fp32 of the weight's shape (a bias
+    without a weight: [D])."""
+    lib = load_library()
+    dev, T, G, D, dt = _norm_sizes(x, weight)
+    _check(dy, "dy", dt, x.shape, dev)
+    _check(mean, "mean", torch.float32, x.shape[:-1], dev)
+    _check(rstd, "rstd", torch.float32, x.shape[:-1], dev)
+    shape = (D,)
+    if weight is not None:
+        shape = (G, D) if weight.dim() == 2 else (D,)
+        _check(weight, "weight", torch.float32, shape, dev)
+    if dx is not None:
+        _check(dx, "dx", dt, x.shape, dev)
+    sums = weight is not None or bias
+    need = lib.kda_layernorm_bwd_workspace_size(T, G, D, _DTYPES[dt]) if sums else 0
+    with _on(stream):
+        out = {"dx": torch.empty_like(x) if dx is None else dx}
+        if weight is not None:
+            out["dweight"] = torch.empty(shape, dtype=torch.float32, device=dev)
+        if bias:
+            out["dbias"] = torch.empty(shape, dtype=torch.float32, device=dev)
+        ws, ws_bytes, _keep = _workspace(need, workspace, dev)
+    st = lib.kda_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), T, G, D,
+                               _DTYPES[dt], _ptr(out["dx"]), _ptr(out.get("dweight")),
+                               _ptr(out.get("dbias")), ws, ws_bytes, _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_layernorm_bwd")
+    return out
 
 
 def kda_stream_status(stream=None) -> int:

@@ -12,6 +12,10 @@
 #include "kda_chunk_sm100.cuh"
 #include "kda_prologue.cuh"
 #include "kda_backward.cuh"
+#include "kda_linear_simt.cuh"
+#include "kda_linear_decode.cuh"
+#include "kda_rotary.cuh"
+#include "kda_layernorm.cuh"
 
 #include <cuda_runtime.h>
 
@@ -155,7 +159,7 @@ kda_status dispatch_decode(int d, const void *q, const void *k, const void *v,
 
 extern "C" {
 
-int32_t kda_version(void) { return 10100; }
+int32_t kda_version(void) { return 10200; }
 
 const char *kda_status_string(kda_status s) {
     switch (s) {
@@ -437,5 +441,7 @@ kda_status kda_stream_status(void *stream) {
 
 }  // extern "C"
 
+#include "kda_linear_api.cuh"
+#include "kda_layer_api.cuh"
 #include "kda_noalloc.cuh"
 #include "kda_selftest.cuh"

@@ -1,0 +1,155 @@
+// kda_linear_common.cuh -- decayed linear attention: the segment map, the
+// decay sums, and the scan over segment states that every path shares.
+//
+// Per head, with a log-decay g_t <= 0 (one per token, or one constant):
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+// A chunk of C tokens starting from S0, with b_i = g_1 + .. + g_i inside it and
+// D_ij = e^{b_i - b_j} for i >= j:
+//   O  = scale * ( Diag(e^b) Q S0 + (Q K^T . D) V )
+//   S  = e^{b_C} S0 + (Diag(e^{b_C - b}) K)^T V
+// The composition of two stretches of tokens is S -> gamma S + R with a scalar
+// gamma, so a sequence can be cut into segments: every segment's R from a zero
+// start (in parallel), an elementwise scan of the R of one (sequence, head),
+// then every segment's outputs from its true start state (in parallel).
+//
+// Segment map.  Sequence lengths are known on the device only.  A segment is L
+// tokens of one sequence (the last one shorter); segment s of sequence n gets
+// the unit number  start_n / L + n + s.  Because ceil(len / L) <=
+// (start + len) / L - start / L + 1, the numbers of different sequences never
+// meet, the largest is below T_tot / L + N, and a unit finds its sequence by a
+// binary search of cu_seqlens: no table, no launch to build one.  At most N
+// units have no segment and return at once.
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace lin {
+
+struct SegMap {
+    const int32_t *cu;
+    int N;
+    int64_t T_tot;
+    int64_t L;      // tokens of a segment
+    int units;      // T_tot / L + N
+};
+
+struct Segment {
+    int n;                 // sequence
+    int s, count;          // index of the segment, segments of the sequence
+    int64_t t0, t1;        // its tokens
+};
+
+__device__ __forceinline__ int64_t seq_begin(const SegMap &m, int n) {
+    return m.cu == nullptr ? (int64_t)n * (m.T_tot / m.N) : (int64_t)m.cu[n];
+}
+
+__device__ __forceinline__ int64_t unit_base(const SegMap &m, int n) {
+    return seq_begin(m, n) / m.L + n;
+}
+
+// The segments of sequence n; false when its bounds are malformed.  With good
+// bounds every unit of the sequence lies in [0, m.units).
+__device__ __forceinline__ bool seq_segments(const SegMap &m, int n, int64_t &start, int64_t &end,
+                                             int &base, int &count) {
+    if (!seq_bounds(m.cu, n, m.N, m.T_tot, start, end)) return false;
+    base = (int)(start / m.L + n);
+    count = end > start ? (int)((end - start + m.L - 1) / m.L) : 1;
+    return true;
+}
+
+// The segment of unit u; false when it has none.
+__device__ __forceinline__ bool find_segment(const SegMap &m, int u, Segment &g) {
+    int lo = 0, hi = m.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (unit_base(m, mid) <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    int64_t start, end;
+    int base;
+    g.n = lo;
+    if (!seq_segments(m, lo, start, end, base, g.count)) return false;
+    g.s = u - base;
+    if (g.s < 0 || g.s >= g.count) return false;
+    g.t0 = start + (int64_t)g.s * m.L;
+    g.t1 = g.t0 + m.L < end ? g.t0 + m.L : end;
+    return true;
+}
+
+// The whole of cu_seqlens is checked by one block (every other access relies on
+// the bounds of its own sequence alone): a descent between sequences that no
+// unit looks at is reported too.
+__device__ __forceinline__ void check_seqlens(const SegMap &m) {
+    if (m.cu == nullptr) return;
+    bool ok = true;
+    for (int i = threadIdx.x; i < m.N; i += blockDim.x) ok = ok && m.cu[i] <= m.cu[i + 1];
+    if (threadIdx.x == 0) ok = ok && m.cu[0] == 0 && (int64_t)m.cu[m.N] == m.T_tot;
+    if (!ok) raise_error(kErrSeqlens);
+}
+
+// One log-decay.  Anything below -1e4 forgets everything in every format, and a
+// finite stand-in for -inf keeps differences of sums free of inf - inf; NaN stays.
+__device__ __forceinline__ float clamp_decay(float g) {
+    return g < -1e4f ? -1e4f : g;
+}
+
+__device__ __forceinline__ float load_decay(const float *g, int per_token, int64_t t, int h, int H) {
+    return clamp_decay(per_token ? g[(size_t)t * H + h] : g[h]);
+}
+
+// Inclusive sum over the lanes of a warp, in fp64: sums of up to C log-decays
+// are subtracted from one another, and fp32 would leave the differences between
+// tokens behind a strong decay with its rounding error.
+__device__ __forceinline__ double warp_scan(double x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+// Scan over the segments of one (sequence, head): on entry ws[u][h] holds the
+// segment's R, on return the state it starts from (forward) or the gradient of
+// the state it ends in (reverse).  Elementwise, so bound by memory: one read and
+// one write of each R.  grid (elements / 1024, H, N); a thread owns 4 elements
+// and prefetches the next segment's R before it needs it.
+constexpr int kScanThreads = 256;
+
+template <bool kReverse>
+__global__ void __launch_bounds__(kScanThreads)
+segment_scan_kernel(SegMap m, int H, int dd, const float *init, const float *__restrict__ total,
+                    float *ws) {
+    const int h = blockIdx.y;
+    const int e = (blockIdx.x * kScanThreads + threadIdx.x) * 4;
+    if (e >= dd) return;
+    for (int n = blockIdx.z; n < m.N; n += gridDim.z) {
+        int64_t start, end;
+        int base, count;
+        if (!seq_segments(m, n, start, end, base, count)) continue;
+        float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (init != nullptr)
+            S = *reinterpret_cast<const float4 *>(init + ((size_t)n * H + h) * dd + e);
+        const int step = kReverse ? -1 : 1;
+        int u = kReverse ? base + count - 1 : base;
+        // the last segment in scan order has no R: nothing starts from its end
+        float4 next = S;
+        if (count > 1) next = *reinterpret_cast<const float4 *>(ws + ((size_t)u * H + h) * dd + e);
+        for (int i = 0; i < count; ++i, u += step) {
+            const float4 R = next;
+            if (i + 2 < count)
+                next = *reinterpret_cast<const float4 *>(ws + ((size_t)(u + step) * H + h) * dd + e);
+            *reinterpret_cast<float4 *>(ws + ((size_t)u * H + h) * dd + e) = S;
+            if (i + 1 < count) {
+                const float a = total[(size_t)u * H + h];
+                S.x = fmaf(a, S.x, R.x); S.y = fmaf(a, S.y, R.y);
+                S.z = fmaf(a, S.z, R.z); S.w = fmaf(a, S.w, R.w);
+            }
+        }
+    }
+}
+
+}  // namespace lin
+}  // namespace kda

@@ -1,0 +1,546 @@
+// kda_linear_simt.cuh -- decayed linear attention on CUDA cores, all in fp32:
+// segment states, outputs, and the two halves of the gradient.
+//
+// Serves fp32 inputs (held to 1e-5) and head sizes below 128.  32-token
+// chunks: their products and the state update cost the same order of work, and
+// the chunk's tiles and the state fit shared memory at every head size.  Every
+// product is a register tile over operands in shared memory whose rows are
+// padded by one float, so that both row-wise and column-wise reads are free of
+// bank conflicts; shared-memory loads bound it.
+//
+// Gradient of L = <dO, O> + <dhT, hT>, per chunk with E = dL/dS at its end:
+//   P = Q K^T . D scale,   dP = dO V^T,   dA = dP . D scale
+//   dQ = dA K + Diag(scale e^b) dO S0^T
+//   dK = dA^T Q + Diag(e^{b_C - b}) V E^T
+//   dV = P^T dO + Diag(e^{b_C - b}) K E
+//   dL/dS0 = e^{b_C} E + (Diag(scale e^b) Q)^T dO
+//   dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <S_end, E_end>
+// S is needed for dQ alone and E for dK, dV alone, so one kernel walks forward
+// with S (dQ) and one backward with E (dK, dV, dg): no state is stored per chunk.
+// q_i . dq_i and k_i . dk_i are formed from the fp32 products (the part inside
+// the chunk as row and column sums of P . dP), not from rounded dq, dk.
+#pragma once
+
+#include "kda_linear_common.cuh"
+
+namespace kda {
+namespace lin {
+
+constexpr int kC = 32;                 // tokens of a chunk
+constexpr int kThreads = 256;
+
+// A register tile of an M x N product over 256 threads: lanes run along N.
+template <int M, int N>
+struct Tile {
+    static constexpr int kNT = N < 32 ? N : 32;
+    static constexpr int kRows = kThreads / kNT;       // rows covered at once
+    static constexpr int kI = M / kRows, kJ = N / kNT;
+    static_assert(M % kRows == 0 && N % kNT == 0, "tile");
+    float v[kI][kJ];
+    static __device__ __forceinline__ int m(int i) { return threadIdx.x / kNT + i * kRows; }
+    static __device__ __forceinline__ int n(int j) { return threadIdx.x % kNT + j * kNT; }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kI; ++i)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) v[i][j] = 0.f;
+    }
+    // v += A B, A(m, k) = A[m lda + k] (or A[k lda + m] if TA), B alike.
+    template <int K, bool TA, bool TB>
+    __device__ __forceinline__ void mac(const float *A, int lda, const float *B, int ldb) {
+#pragma unroll 4
+        for (int k = 0; k < K; ++k) {
+            float a[kI], b[kJ];
+#pragma unroll
+            for (int i = 0; i < kI; ++i) a[i] = TA ? A[k * lda + m(i)] : A[m(i) * lda + k];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) b[j] = TB ? B[n(j) * ldb + k] : B[k * ldb + n(j)];
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) v[i][j] = fmaf(a[i], b[j], v[i][j]);
+        }
+    }
+};
+
+// Sum over the kNT lanes that share a row of a tile.
+template <int NT>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = NT / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// [kC][W] tile of rows t0 .. t0 + len of x [T, heads, D], columns c0 .. c0 + W,
+// zero behind len (a row of zeros with log-decay 0 leaves every result alone).
+template <typename T, int W>
+__device__ __forceinline__ void load_tile(float *dst, const T *x, int64_t t0, int len, int heads,
+                                          int head, int D, int c0) {
+    for (int e = threadIdx.x; e < kC * W; e += kThreads) {
+        const int r = e / W, c = e % W;
+        dst[r * (W + 1) + c] =
+            r < len ? IO<T>::ld(x + ((size_t)(t0 + r) * heads + head) * D + c0 + c) : 0.f;
+    }
+}
+
+// Decay sums of a chunk by warp 0: b_i in fp64 (b[i]), total b[kC - 1].
+__device__ __forceinline__ void chunk_decays(double *b, const float *g, int per_token, int64_t t0,
+                                             int len, int h, int H) {
+    if (threadIdx.x < 32) {
+        const int i = threadIdx.x;
+        b[i] = warp_scan(i < len ? (double)load_decay(g, per_token, t0 + i, h, H) : 0.0);
+    }
+}
+
+// ------------------------------------------------------- segment states
+// Forward: R = sum_j e^{b_end - b_j} k_j v_j^T over the segment (skipped for the
+// last segment of a sequence).  Reverse: R = sum_i scale e^{b_i} q_i dO_i^T, b
+// counted from the segment's start (skipped for the first).
+template <int D>
+struct StateSmem {
+    static constexpr int kW = D < 64 ? D : 64;         // value columns of a block
+    float x[kC * (D + 1)], y[kC * (kW + 1)];
+    double b[kC];
+};
+
+template <typename T, int D, bool kReverse>
+__global__ void __launch_bounds__(kThreads)
+state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__restrict__ g,
+             int per_token, SegMap m, int Hk, int H, float scale, float *__restrict__ ws,
+             float *__restrict__ total) {
+    using Sm = StateSmem<D>;
+    constexpr int W = Sm::kW;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Sm &sm = *reinterpret_cast<Sm *>(raw);
+    const int u = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * W;
+    Segment sg;
+    if (!find_segment(m, u, sg)) return;
+    if (sg.s == (kReverse ? 0 : sg.count - 1)) return;
+    Tile<D, W> S;
+    S.zero();
+    double sum = 0.0;
+    const int64_t len = sg.t1 - sg.t0;
+    const int64_t chunks = (len + kC - 1) / kC;
+    for (int64_t c = 0; c < chunks; ++c) {
+        const int64_t t = sg.t0 + (kReverse ? chunks - 1 - c : c) * kC;
+        const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
+        __syncthreads();
+        load_tile<T, D>(sm.x, x, t, L, Hk, h / (H / Hk), D, 0);
+        load_tile<T, W>(sm.y, y, t, L, H, h, D, c0);
+        chunk_decays(sm.b, g, per_token, t, L, h, H);
+        __syncthreads();
+        const double tot = sm.b[kC - 1];
+        sum += tot;
+        for (int e = threadIdx.x; e < kC * W; e += kThreads) {
+            const int r = e / W;
+            sm.y[r * (W + 1) + e % W] *=
+                kReverse ? scale * expf((float)sm.b[r]) : expf((float)(tot - sm.b[r]));
+        }
+        const float a = expf((float)tot);
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j) S.v[i][j] *= a;
+        __syncthreads();
+        S.template mac<kC, true, false>(sm.x, D + 1, sm.y, W + 1);
+    }
+    float *out = ws + ((size_t)u * H + h) * D * D + c0;
+#pragma unroll
+    for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+        for (int j = 0; j < S.kJ; ++j) out[(size_t)S.m(i) * D + S.n(j)] = S.v[i][j];
+    if (c0 == 0 && threadIdx.x == 0) total[(size_t)u * H + h] = expf((float)sum);
+}
+
+// -------------------------------------------------------------- outputs
+template <int D>
+struct OutSmem {
+    static constexpr int kW = D < 64 ? D : 64;
+    float S[D * (kW + 1)];
+    float q[kC * (D + 1)], k[kC * (D + 1)], v[kC * (kW + 1)], P[kC * (kC + 1)];
+    double b[kC];
+};
+
+// grid (units, H, D / kW): value columns are independent, so a head is split
+// over blocks of 64 columns (the chunk's 32 x 32 products are formed in each).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+           const float *__restrict__ g, int per_token, const float *h0, SegMap m, int Hk, int H,
+           float scale, const float *__restrict__ ws, T *__restrict__ o, float *hT) {
+    using Sm = OutSmem<D>;
+    constexpr int W = Sm::kW;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Sm &sm = *reinterpret_cast<Sm *>(raw);
+    const int u = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * W;
+    if (u == 0 && h == 0 && c0 == 0) check_seqlens(m);
+    Segment sg;
+    if (!find_segment(m, u, sg)) return;
+    const float *from = ws != nullptr ? ws + ((size_t)u * H + h) * D * D
+                        : h0 != nullptr ? h0 + ((size_t)sg.n * H + h) * D * D : nullptr;
+    Tile<D, W> S;
+#pragma unroll
+    for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+        for (int j = 0; j < S.kJ; ++j) {
+            S.v[i][j] = from != nullptr ? from[(size_t)S.m(i) * D + c0 + S.n(j)] : 0.f;
+            sm.S[S.m(i) * (W + 1) + S.n(j)] = S.v[i][j];
+        }
+    for (int64_t t = sg.t0; t < sg.t1; t += kC) {
+        const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
+        __syncthreads();
+        load_tile<T, D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
+        load_tile<T, D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
+        load_tile<T, W>(sm.v, v, t, L, H, h, D, c0);
+        chunk_decays(sm.b, g, per_token, t, L, h, H);
+        __syncthreads();
+        Tile<kC, kC> P;
+        P.zero();
+        P.template mac<D, false, true>(sm.q, D + 1, sm.k, D + 1);
+#pragma unroll
+        for (int i = 0; i < P.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < P.kJ; ++j) {
+                const int r = P.m(i), c = P.n(j);
+                sm.P[r * (kC + 1) + c] = r >= c ? P.v[i][j] * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
+            }
+        Tile<kC, W> O;
+        O.zero();
+        O.template mac<D, false, false>(sm.q, D + 1, sm.S, W + 1);
+#pragma unroll
+        for (int i = 0; i < O.kI; ++i) {
+            const float a = expf((float)sm.b[O.m(i)]);
+#pragma unroll
+            for (int j = 0; j < O.kJ; ++j) O.v[i][j] *= a;
+        }
+        __syncthreads();
+        O.template mac<kC, false, false>(sm.P, kC + 1, sm.v, W + 1);
+#pragma unroll
+        for (int i = 0; i < O.kI; ++i)
+            if (O.m(i) < L)
+#pragma unroll
+                for (int j = 0; j < O.kJ; ++j)
+                    IO<T>::st(o + ((size_t)(t + O.m(i)) * H + h) * D + c0 + O.n(j), O.v[i][j] * scale);
+        __syncthreads();
+        const double tot = sm.b[kC - 1];
+        for (int e = threadIdx.x; e < kC * W; e += kThreads)
+            sm.v[e / W * (W + 1) + e % W] *= expf((float)(tot - sm.b[e / W]));
+        const float a = expf((float)tot);
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j) S.v[i][j] *= a;
+        __syncthreads();
+        S.template mac<kC, true, false>(sm.k, D + 1, sm.v, W + 1);
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (W + 1) + S.n(j)] = S.v[i][j];
+    }
+    if (hT != nullptr && sg.s == sg.count - 1) {
+        float *out = hT + ((size_t)sg.n * H + h) * D * D + c0;
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j) out[(size_t)S.m(i) * D + S.n(j)] = S.v[i][j];
+    }
+}
+
+// ------------------------------------------------------------- gradient
+template <int D>
+struct GradSmem {
+    float S[D * (D + 1)];                              // S (dQ) or E (dK, dV)
+    float q[kC * (D + 1)], k[kC * (D + 1)], v[kC * (D + 1)], dO[kC * (D + 1)];
+    float P[kC * (kC + 1)], A[kC * (kC + 1)];
+    double b[kC];
+    float r[kC];
+    double red[kThreads / 32];
+};
+
+// Loads a chunk and forms P = (Q K^T . D) scale and dA = (dO V^T . D) scale in
+// shared memory; kW: P is replaced by W = P . dO V^T.
+template <typename T, int D, bool kW>
+__device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T *k, const T *v,
+                                           const T *dO, const float *g, int per_token, int64_t t,
+                                           int L, int Hk, int H, int h, float scale) {
+    load_tile<T, D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
+    load_tile<T, D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
+    load_tile<T, D>(sm.v, v, t, L, H, h, D, 0);
+    load_tile<T, D>(sm.dO, dO, t, L, H, h, D, 0);
+    chunk_decays(sm.b, g, per_token, t, L, h, H);
+    __syncthreads();
+    Tile<kC, kC> P, dP;
+    P.zero();
+    dP.zero();
+    P.template mac<D, false, true>(sm.q, D + 1, sm.k, D + 1);
+    dP.template mac<D, false, true>(sm.dO, D + 1, sm.v, D + 1);
+#pragma unroll
+    for (int i = 0; i < P.kI; ++i)
+#pragma unroll
+        for (int j = 0; j < P.kJ; ++j) {
+            const int r = P.m(i), c = P.n(j);
+            const float e = r >= c ? scale * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
+            const float p = P.v[i][j] * e;
+            sm.P[r * (kC + 1) + c] = r >= c ? (kW ? p * dP.v[i][j] : p) : 0.f;
+            sm.A[r * (kC + 1) + c] = r >= c ? dP.v[i][j] * e : 0.f;
+        }
+}
+
+// A gradient row of a head that shares q and k with others goes out in fp32 (to
+// be summed over the group), else rounded.
+template <typename T>
+__device__ __forceinline__ void store_shared(T *out, float *part, size_t e, float x) {
+    if (part != nullptr) part[e] = x;
+    else IO<T>::st(out + e, x);
+}
+
+// dQ, the decay term of every row (rowsum W - colsum W + q . dq from the state),
+// and <S_end, E_end> of the segment.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+              const T *__restrict__ dO, const float *__restrict__ g, int per_token,
+              const float *__restrict__ h0, const float *__restrict__ dhT, SegMap m, int Hk, int H,
+              float scale, const float *__restrict__ wsS, const float *__restrict__ wsE,
+              T *__restrict__ dq, float *__restrict__ part, float *__restrict__ term,
+              double *__restrict__ anchor) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    GradSmem<D> &sm = *reinterpret_cast<GradSmem<D> *>(raw);
+    const int u = blockIdx.x, h = blockIdx.y;
+    if (u == 0 && h == 0) check_seqlens(m);
+    Segment sg;
+    if (!find_segment(m, u, sg)) return;
+    const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
+    const float *from = wsS != nullptr ? wsS + seg : h0 != nullptr ? h0 + seq : nullptr;
+    Tile<D, D> S;
+#pragma unroll
+    for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+        for (int j = 0; j < S.kJ; ++j) {
+            S.v[i][j] = from != nullptr ? from[(size_t)S.m(i) * D + S.n(j)] : 0.f;
+            sm.S[S.m(i) * (D + 1) + S.n(j)] = S.v[i][j];
+        }
+    for (int64_t t = sg.t0; t < sg.t1; t += kC) {
+        const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
+        __syncthreads();
+        grad_chunk<T, D, true>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
+        Tile<kC, D> X;                                 // dO S^T
+        X.zero();
+        X.template mac<D, false, true>(sm.dO, D + 1, sm.S, D + 1);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < X.kI; ++i) {
+            const int r = X.m(i);
+            const float a = scale * expf((float)sm.b[r]);
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < X.kJ; ++j) {
+                X.v[i][j] *= a;
+                s = fmaf(X.v[i][j], sm.q[r * (D + 1) + X.n(j)], s);
+            }
+            s = row_sum<X.kNT>(s);
+            if (threadIdx.x % X.kNT == 0) sm.r[r] = s;
+        }
+        X.template mac<kC, false, false>(sm.A, kC + 1, sm.k, D + 1);
+#pragma unroll
+        for (int i = 0; i < X.kI; ++i)
+            if (X.m(i) < L)
+#pragma unroll
+                for (int j = 0; j < X.kJ; ++j) {
+                    const size_t row = (size_t)(t + X.m(i)) * H + h;
+                    store_shared(dq, part, row * D + X.n(j), X.v[i][j]);
+                }
+        const double tot = sm.b[kC - 1];
+        for (int e = threadIdx.x; e < kC * D; e += kThreads)
+            sm.v[e / D * (D + 1) + e % D] *= expf((float)(tot - sm.b[e / D]));
+        const float a = expf((float)tot);
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j) S.v[i][j] *= a;
+        __syncthreads();
+        if (threadIdx.x < L) {
+            float s = sm.r[threadIdx.x];
+            for (int c = 0; c < kC; ++c)
+                s += sm.P[threadIdx.x * (kC + 1) + c] - sm.P[c * (kC + 1) + threadIdx.x];
+            term[(size_t)(t + threadIdx.x) * H + h] = s;
+        }
+        S.template mac<kC, true, false>(sm.k, D + 1, sm.v, D + 1);
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (D + 1) + S.n(j)] = S.v[i][j];
+    }
+    const float *to = wsE != nullptr ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
+    double s = 0.0;
+    if (to != nullptr)
+#pragma unroll
+        for (int i = 0; i < S.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < S.kJ; ++j)
+                s += (double)S.v[i][j] * (double)to[(size_t)S.m(i) * D + S.n(j)];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (threadIdx.x % 32 == 0) sm.red[threadIdx.x / 32] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = 0.0;
+        for (int i = 0; i < kThreads / 32; ++i) s += sm.red[i];
+        anchor[(size_t)u * H + h] = s;
+    }
+}
+
+// dK, dV, dg and dh0, chunks last to first.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+               const T *__restrict__ dO, const float *__restrict__ g, int per_token,
+               const float *__restrict__ dhT, SegMap m, int Hk, int H, float scale,
+               const float *__restrict__ wsE, const float *__restrict__ term,
+               const double *__restrict__ anchor, T *__restrict__ dk, float *__restrict__ part,
+               T *__restrict__ dv, float *__restrict__ dg, double *__restrict__ head_sum,
+               float *__restrict__ dh0) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    GradSmem<D> &sm = *reinterpret_cast<GradSmem<D> *>(raw);
+    const int u = blockIdx.x, h = blockIdx.y;
+    Segment sg;
+    if (!find_segment(m, u, sg)) {
+        if (!per_token && threadIdx.x == 0) head_sum[(size_t)u * H + h] = 0.0;
+        return;
+    }
+    const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
+    const float *from = wsE != nullptr ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
+    Tile<D, D> E;
+#pragma unroll
+    for (int i = 0; i < E.kI; ++i)
+#pragma unroll
+        for (int j = 0; j < E.kJ; ++j) {
+            E.v[i][j] = from != nullptr ? from[(size_t)E.m(i) * D + E.n(j)] : 0.f;
+            sm.S[E.m(i) * (D + 1) + E.n(j)] = E.v[i][j];
+        }
+    double carry = anchor[(size_t)u * H + h], sum = 0.0;   // warp 0
+    const int64_t chunks = (sg.t1 - sg.t0 + kC - 1) / kC;
+    for (int64_t c = chunks - 1; c >= 0; --c) {
+        const int64_t t = sg.t0 + c * kC;
+        const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
+        __syncthreads();
+        grad_chunk<T, D, false>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
+        const double tot = sm.b[kC - 1];
+        Tile<kC, D> X;                                 // V E^T
+        X.zero();
+        X.template mac<D, false, true>(sm.v, D + 1, sm.S, D + 1);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < X.kI; ++i) {
+            const int r = X.m(i);
+            const float a = expf((float)(tot - sm.b[r]));
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < X.kJ; ++j) {
+                X.v[i][j] *= a;
+                s = fmaf(X.v[i][j], sm.k[r * (D + 1) + X.n(j)], s);
+            }
+            s = row_sum<X.kNT>(s);
+            if (threadIdx.x % X.kNT == 0) sm.r[r] = s;
+        }
+        X.template mac<kC, true, false>(sm.A, kC + 1, sm.q, D + 1);
+#pragma unroll
+        for (int i = 0; i < X.kI; ++i)
+            if (X.m(i) < L)
+#pragma unroll
+                for (int j = 0; j < X.kJ; ++j) {
+                    const size_t row = (size_t)(t + X.m(i)) * H + h;
+                    store_shared(dk, part, row * D + X.n(j), X.v[i][j]);
+                }
+        X.zero();                                      // K E
+        X.template mac<D, false, false>(sm.k, D + 1, sm.S, D + 1);
+#pragma unroll
+        for (int i = 0; i < X.kI; ++i) {
+            const float a = expf((float)(tot - sm.b[X.m(i)]));
+#pragma unroll
+            for (int j = 0; j < X.kJ; ++j) X.v[i][j] *= a;
+        }
+        X.template mac<kC, true, false>(sm.P, kC + 1, sm.dO, D + 1);
+#pragma unroll
+        for (int i = 0; i < X.kI; ++i)
+            if (X.m(i) < L)
+#pragma unroll
+                for (int j = 0; j < X.kJ; ++j)
+                    IO<T>::st(dv + ((size_t)(t + X.m(i)) * H + h) * D + X.n(j), X.v[i][j]);
+        __syncthreads();
+        for (int e = threadIdx.x; e < kC * D; e += kThreads)
+            sm.dO[e / D * (D + 1) + e % D] *= scale * expf((float)sm.b[e / D]);
+        if (threadIdx.x < 32) {                        // sums from the chunk's end
+            const int i = threadIdx.x, r = 31 - i;
+            double x = 0.0;
+            if (r < L) x = (double)term[(size_t)(t + r) * H + h] - (double)sm.r[r];
+            x = warp_scan(x) + carry;
+            if (r < L) {
+                if (per_token) dg[(size_t)(t + r) * H + h] = (float)x;
+                sum += x;
+            }
+            carry = __shfl_sync(0xffffffffu, x, 31);
+        }
+        const float a = expf((float)tot);
+#pragma unroll
+        for (int i = 0; i < E.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < E.kJ; ++j) E.v[i][j] *= a;
+        __syncthreads();
+        E.template mac<kC, true, false>(sm.q, D + 1, sm.dO, D + 1);
+#pragma unroll
+        for (int i = 0; i < E.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < E.kJ; ++j) sm.S[E.m(i) * (D + 1) + E.n(j)] = E.v[i][j];
+    }
+    if (!per_token && threadIdx.x < 32) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (threadIdx.x == 0) head_sum[(size_t)u * H + h] = sum;
+    }
+    if (dh0 != nullptr && sg.s == 0) {
+        float *out = dh0 + seq;
+#pragma unroll
+        for (int i = 0; i < E.kI; ++i)
+#pragma unroll
+            for (int j = 0; j < E.kJ; ++j) out[(size_t)E.m(i) * D + E.n(j)] = E.v[i][j];
+    }
+}
+
+// out[t][hk][c] = sum over the group of part[t][hk r + i][c], in fp32 and in the
+// order of the heads; a thread owns 4 channels of one (t, hk).
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+group_sum_kernel(const float *__restrict__ part, T *__restrict__ out, int64_t rows, int rep, int D) {
+    const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (e >= rows * D) return;
+    const int64_t row = e / D;
+    const float *p = part + row * rep * D + e % D;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < rep; ++i) {
+        const float4 x = *reinterpret_cast<const float4 *>(p + (size_t)i * D);
+        s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    IO<T>::st(out + e, s.x);
+    IO<T>::st(out + e + 1, s.y);
+    IO<T>::st(out + e + 2, s.z);
+    IO<T>::st(out + e + 3, s.w);
+}
+
+// dg[h] of a constant decay: the units' sums in order.
+__global__ void __launch_bounds__(kThreads)
+head_sum_kernel(const double *__restrict__ head_sum, float *__restrict__ dg, int units, int H) {
+    __shared__ double red[kThreads];
+    double s = 0.0;
+    for (int u = threadIdx.x; u < units; u += kThreads) s += head_sum[(size_t)u * H + blockIdx.x];
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int o = kThreads / 2; o > 0; o >>= 1) {
+        if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dg[blockIdx.x] = (float)red[0];
+}
+
+}  // namespace lin
+}  // namespace kda

@@ -252,6 +252,154 @@ KDA_API kda_status kda_prologue(const void *xq, const void *xk, const void *xv,
                                 void *k, void *v, void *beta, void *stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrence without the
+ * delta rule and with one retention per head instead of one per key channel,
+ *
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t
+ *
+ *   q, k        device [T_tot, Hk, d]      (dt)   H % Hk = 0: head h reads the
+ *   v           device [T_tot, H, d]       (dt)   q and k of head h / (H / Hk)
+ *   g           device fp32 log-decays, natural logarithm: [T_tot, H] with
+ *               g_per_token != 0, else [H], one constant for each head.
+ *               g <= 0 in use; -inf forgets exactly; a positive g is growth,
+ *               and the caller's concern.  4-byte alignment is enough for g and
+ *               dg (and for inv_freq, positions, mean and rstd further down).
+ *   h0, hT      device [N, H, d, d] fp32 states [key][value], or NULL (zero
+ *               start; not written); hT may be h0 (in-place carry)
+ *   o           device [T_tot, H, d]       (dt)
+ *   cu_seqlens, N, T_tot                   as for kda_chunk_fwd
+ *   scale       finite
+ *   workspace   kda_linear_chunk_fwd_workspace_size() bytes, 256-byte aligned
+ *               (NULL when that is 0): the states between segments
+ *
+ * dt KDA_BF16 or KDA_FP32, d in {16, 32, 64, 128}, H <= 65535, N * H below
+ * 2^31.  The decay sums are formed in fp64, states and every product's sum in
+ * fp32.  q, k, v are finite: a NaN or an infinity at one token may reach the
+ * outputs of the tokens of its 128-token chunk that come before it.  Status as
+ * for kda_chunk_fwd.
+ */
+KDA_API size_t kda_linear_chunk_fwd_workspace_size(int32_t N, int64_t T_tot, int32_t H, int32_t d,
+                                                   kda_dtype dt);
+KDA_API kda_status kda_linear_chunk_fwd(const void *q, const void *k, const void *v,
+                                        const float *g, const float *h0,
+                                        const int32_t *cu_seqlens, int32_t N, int64_t T_tot,
+                                        int32_t Hk, int32_t H, int32_t d, kda_dtype dt,
+                                        int32_t g_per_token, float scale, void *o, float *hT,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of it for B sequences: q, k [B, Hk, d], v, o [B, H, d] (dt), g
+ * fp32 [B, H] or [H], S [B, H, d, d] fp32 read and overwritten.
+ */
+KDA_API kda_status kda_linear_decode_step(const void *q, const void *k, const void *v,
+                                          const float *g, float *S, void *o, int32_t B, int32_t Hk,
+                                          int32_t H, int32_t d, kda_dtype dt, int32_t g_per_token,
+                                          float scale, void *stream);
+
+/*
+ * Gradient of kda_linear_chunk_fwd for L = <dO, o> + <dhT, hT>; the forward's
+ * outputs are not needed.
+ *
+ *   dO          device [T_tot, H, d]  (dt)
+ *   dhT         device [N, H, d, d] fp32, or NULL (zero)
+ *   dq, dk      device [T_tot, Hk, d] (dt)  summed over the heads that share a row
+ *   dv          device [T_tot, H, d]  (dt)
+ *   dg          device fp32, of g's shape: [T_tot, H], or [H] summed over the tokens
+ *   dh0         device [N, H, d, d] fp32, or NULL (not written)
+ *   workspace   kda_linear_chunk_bwd_workspace_size() bytes, 256-byte aligned
+ */
+KDA_API size_t kda_linear_chunk_bwd_workspace_size(int32_t N, int64_t T_tot, int32_t Hk, int32_t H,
+                                                   int32_t d, kda_dtype dt);
+KDA_API kda_status kda_linear_chunk_bwd(const void *q, const void *k, const void *v,
+                                        const float *g, const float *h0,
+                                        const int32_t *cu_seqlens, int32_t N, int64_t T_tot,
+                                        int32_t Hk, int32_t H, int32_t d, kda_dtype dt,
+                                        int32_t g_per_token, float scale, const void *dO,
+                                        const float *dhT, void *dq, void *dk, void *dv, float *dg,
+                                        float *dh0, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/*
+ * Rotary positions of q and k: over the first `rot` channels of every head,
+ * pair i turns by pos * inv_freq[i],
+ *
+ *   (x, y) -> scale (x cos - y sin, x sin + y cos)
+ *
+ * The other channels are copied.  Pairs are (i, i + rot / 2), or the
+ * neighbours (2 i, 2 i + 1) with interleaved != 0.  inverse != 0 turns by the
+ * negated angle: with it, the gradients of the outputs give those of the inputs.
+ * Angles are exact to 2e-7 rad for every 32-bit position.
+ *
+ *   q, q_out    device, Hq heads of d (dt) at stride q_stride / q_out_stride
+ *               elements between tokens (at least Hq * d); q_out may be q with
+ *               the same stride (in place), and may not overlap it otherwise
+ *   k, k_out    the same with Hk heads; Hk = 0 leaves k out
+ *   inv_freq    device fp32 [rot / 2]
+ *   positions   device int32 [T_tot], or NULL: the index of the token in its
+ *               sequence by cu_seqlens / N (as for kda_chunk_fwd)
+ *
+ * rot even, rot <= d, rot <= 256, d <= 1024, T_tot < 2^31; dt KDA_BF16 or KDA_FP32;
+ * fp32 arithmetic, one rounding.
+ */
+KDA_API kda_status kda_rotary(const void *q, const void *k, const float *inv_freq,
+                              const int32_t *positions, const int32_t *cu_seqlens, int32_t N,
+                              int64_t T_tot, int32_t Hq, int32_t Hk, int32_t d, int32_t rot,
+                              kda_dtype dt, int32_t interleaved, int32_t inverse, float scale,
+                              int64_t q_stride, int64_t k_stride, void *q_out, void *k_out,
+                              int64_t q_out_stride, int64_t k_out_stride, void *stream);
+
+typedef enum {
+    KDA_ROPE_NONE = 0,   /* base^(-2 i / rot)                                    */
+    KDA_ROPE_LINEAR = 1, /* divided by factor: positions interpolated            */
+    KDA_ROPE_BASE = 2,   /* base * factor^(rot / (rot - 2)): the slowest pair by
+                            factor, the fastest not at all                       */
+    KDA_ROPE_PARTS = 3   /* pairs of more than beta_fast turns over
+                            original_length keep their frequency, those of less
+                            than beta_slow divide it by factor, a linear ramp
+                            between; scale = 1 + 0.1 ln(factor)                  */
+} kda_rope_scaling;
+
+/*
+ * The frequencies of kda_rotary and its scale (1 but for KDA_ROPE_PARTS), into
+ * HOST memory: inv_freq [rot / 2], scale [1].  A pure host function.
+ */
+KDA_API kda_status kda_rotary_frequencies(int32_t rot, double base, kda_rope_scaling scaling,
+                                          double factor, double original_length, double beta_fast,
+                                          double beta_slow, float *inv_freq, float *scale);
+
+/*
+ * Layer norm of rows of D values: y = (x - mean) rstd weight + bias, with
+ * rstd = (variance + eps)^(-1/2).  Rows are [T, G, D]; row (t, g) takes row g
+ * of the weights, so G = 1 is the norm of a stream and G = H that of each
+ * head's output.
+ *
+ *   x, y        device [T, G, D] (dt); y may be x
+ *   weight      device fp32 [G, D], or NULL (ones)
+ *   bias        device fp32 [G, D], or NULL (zeros)
+ *   mean, rstd  device fp32 [T, G], outputs (what the gradient needs)
+ *
+ * D <= 8192; eps finite and >= 0; dt KDA_BF16 or KDA_FP32; statistics in fp32.
+ */
+KDA_API kda_status kda_layernorm_fwd(const void *x, const float *weight, const float *bias,
+                                     int64_t T, int32_t G, int32_t D, kda_dtype dt, float eps,
+                                     void *y, float *mean, float *rstd, void *stream);
+
+/*
+ * Its gradient: dx from dy, x, mean, rstd and weight; dweight and dbias
+ * [G, D] fp32 (each may be NULL), summed over the T rows of each g in an order
+ * that depends on the sizes alone.  dx may be dy.
+ *
+ *   workspace   kda_layernorm_bwd_workspace_size() bytes, 256-byte aligned; not
+ *               needed when dweight and dbias are both NULL
+ */
+KDA_API size_t kda_layernorm_bwd_workspace_size(int64_t T, int32_t G, int32_t D, kda_dtype dt);
+KDA_API kda_status kda_layernorm_bwd(const void *dy, const void *x, const float *mean,
+                                     const float *rstd, const float *weight, int64_t T, int32_t G,
+                                     int32_t D, kda_dtype dt, void *dx, float *dweight,
+                                     float *dbias, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/*
  * kda_chunk_fwd without a caller-provided workspace, for callers that cannot
  * allocate device memory: a serving engine that has reserved nearly all of
  * the GPU's memory for its own caches, a plugin whose host owns the
