@@ -14,6 +14,7 @@
 #include "kda_backward.cuh"
 #include "kda_linear_simt.cuh"
 #include "kda_linear_decode.cuh"
+#include "kda_linear_sm100.cuh"
 #include "kda_rotary.cuh"
 #include "kda_layernorm.cuh"
 

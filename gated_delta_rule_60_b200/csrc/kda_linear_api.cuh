@@ -43,9 +43,46 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
     return p;
 }
 
-inline int64_t fwd_length(int32_t N, int64_t T_tot, int32_t H, int32_t d) {
-    return segment_length(N, false, T_tot, (int64_t)H * (d < 64 ? 1 : d / 64), kC);
+// The tensor-core kernels: one block an SM, a chunk of 128 tokens takes about
+// 1.7 us there, and 0.9 us where only states are wanted.
+inline bool tensor_path(int32_t d, kda_dtype dt) { return d == 128 && dt == KDA_BF16; }
+
+// Equal lengths: the number of segments that minimises the waves of both passes
+// (the first over all segments but the last) and the two further launches.
+// Lengths that the host does not know: an SM's even share of the tokens, which
+// bounds what one long sequence can leave over.
+inline int64_t tensor_length(int32_t N, bool equal, int64_t T_tot, int32_t H) {
+    const int64_t kSMs = 148;
+    if (N <= 0 || T_tot <= 0) return kNoSplit;
+    if (!equal) {
+        int64_t L = (T_tot * H + kSMs - 1) / kSMs;
+        if (L < 1024) L = 1024;
+        L = (L + tc::kTok - 1) / tc::kTok * tc::kTok;
+        return L >= T_tot ? kNoSplit : L;
+    }
+    const int64_t len = (T_tot + N - 1) / N, chunks = (len + tc::kTok - 1) / tc::kTok;
+    auto waves = [&](int64_t blocks) { return (double)((blocks + kSMs - 1) / kSMs); };
+    double best = waves((int64_t)N * H) * 1.7 * (double)chunks;
+    int64_t L = kNoSplit;
+    for (int64_t G = 2; G <= 64 && G * 4 <= chunks; ++G) {
+        const int64_t per = (chunks + G - 1) / G;
+        const double t = ((double)per) * (waves((int64_t)N * H * G) * 1.7 + waves((int64_t)N * H * (G - 1)) * 0.9) + 8.0;
+        if (t < best) {
+            best = t;
+            L = per * tc::kTok;
+        }
+    }
+    return L;
 }
+
+// The workspace query does not know whether cu_seqlens is given: with several
+// sequences it takes the larger of the two plans.
+inline int64_t fwd_length(int32_t N, bool equal, int64_t T_tot, int32_t H, int32_t d, kda_dtype dt) {
+    return tensor_path(d, dt) ? tensor_length(N, equal || N == 1, T_tot, H)
+                              : segment_length(N, false, T_tot, (int64_t)H * (d < 64 ? 1 : d / 64), kC);
+}
+
+inline size_t fwd_bytes(const Plan &p) { return p.state_bytes + p.total_bytes; }
 
 inline int64_t bwd_length(int32_t N, int64_t T_tot, int32_t H, int32_t d) {
     (void)d;
@@ -160,6 +197,45 @@ kda_status fwd_simt(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     return launched();
 }
 
+// [T, heads, 128] maps; with no tokens no tile is copied, and the maps describe
+// a row of hT, which the caller has then given.
+inline kda_status fwd_tensor(const Plan &p, const FwdArgs &a, cudaStream_t s) {
+    const int64_t T = p.map.T_tot;
+    CUtensorMap mq, mk, mv, mo;
+    auto base = [&](const void *x) { return T > 0 ? x : (const void *)a.hT; };
+    const int64_t rows = T > 0 ? T : 1;
+    if (!tc::make_map(&mq, base(a.q), a.Hk, rows) || !tc::make_map(&mk, base(a.k), a.Hk, rows) ||
+        !tc::make_map(&mv, base(a.v), a.H, rows) || !tc::make_map(&mo, base(a.o), a.H, rows))
+        return KDA_ERR_CUDA;
+    tc::Params t;
+    t.g = a.g;
+    t.h0 = a.h0;
+    t.ws = nullptr;
+    t.out = a.hT;
+    t.total = nullptr;
+    t.o = (__nv_bfloat16 *)a.o;
+    t.m = p.map;
+    t.per_token = a.per_token;
+    t.Hk = a.Hk;
+    t.H = a.H;
+    t.scale = a.scale;
+    const unsigned blocks = (unsigned)((int64_t)p.map.units * a.H);
+    if (p.split) {
+        tc::Params r = t;
+        r.out = reinterpret_cast<float *>(a.ws);
+        r.total = reinterpret_cast<float *>(a.ws + p.state_bytes);
+        if (!set_smem(tc::linear_sm100_kernel<true>, tc::kSmem)) return KDA_ERR_CUDA;
+        tc::linear_sm100_kernel<true><<<blocks, tc::kThreads, tc::kSmem, s>>>(mq, mk, mv, mo, r);
+        kda_status st = launched();
+        if (st == KDA_OK) st = launch_scan<false>(p, a.H, tc::kD, a.h0, r.total, r.out, s);
+        if (st != KDA_OK) return st;
+        t.ws = r.out;
+    }
+    if (!set_smem(tc::linear_sm100_kernel<false>, tc::kSmem)) return KDA_ERR_CUDA;
+    tc::linear_sm100_kernel<false><<<blocks, tc::kThreads, tc::kSmem, s>>>(mq, mk, mv, mo, t);
+    return launched();
+}
+
 struct BwdArgs {
     const void *q, *k, *v, *dO;
     const float *g, *h0, *dhT;
@@ -266,11 +342,12 @@ kda_status step(const void *q, const void *k, const void *v, const float *g, int
 
 extern "C" KDA_API size_t kda_linear_chunk_fwd_workspace_size(int32_t N, int64_t T_tot, int32_t H,
                                                               int32_t d, kda_dtype dt) {
-    if (N <= 0 || T_tot < 0 || H <= 0 || !kda::lin::supported_d(d)) return 0;
+    using namespace kda::lin;
+    if (N <= 0 || T_tot < 0 || H <= 0 || !supported_d(d)) return 0;
     if (dt != KDA_BF16 && dt != KDA_FP32) return 0;
-    const kda::lin::Plan p = kda::lin::make_plan(nullptr, N, T_tot, H, d,
-                                                 kda::lin::fwd_length(N, T_tot, H, d));
-    return p.state_bytes + p.total_bytes;
+    const size_t a = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, false, T_tot, H, d, dt)));
+    const size_t b = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, true, T_tot, H, d, dt)));
+    return a > b ? a : b;
 }
 
 extern "C" KDA_API kda_status kda_linear_chunk_fwd(
@@ -286,15 +363,18 @@ extern "C" KDA_API kda_status kda_linear_chunk_fwd(
         return KDA_ERR_INVALID_ARGUMENT;
     if (!kda::lin::ok16(h0) || !kda::lin::ok16(hT)) return KDA_ERR_INVALID_ARGUMENT;
     if (T_tot == 0 && hT == nullptr) return KDA_OK;
-    const kda::lin::Plan p = kda::lin::make_plan(cu_seqlens, N, T_tot, H, d,
-                                                 kda::lin::fwd_length(N, T_tot, H, d));
-    const size_t need = p.state_bytes + p.total_bytes;
+    const kda::lin::Plan p = kda::lin::make_plan(
+        cu_seqlens, N, T_tot, H, d,
+        kda::lin::fwd_length(N, cu_seqlens == nullptr, T_tot, H, d, dt));
+    if ((int64_t)p.map.units * H > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
+    const size_t need = kda_linear_chunk_fwd_workspace_size(N, T_tot, H, d, dt);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
                      (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return KDA_ERR_WORKSPACE;
     const kda::lin::FwdArgs a = {q, k, v, g, h0, g_per_token, Hk, H, scale, o, hT,
                                  (unsigned char *)workspace};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (kda::lin::tensor_path(d, dt)) return kda::lin::fwd_tensor(p, a, s);
     return KDA_LIN_DISPATCH(kda::lin::fwd_simt, dt, d, p, a, s);
 }
 

@@ -129,14 +129,14 @@ segment_scan_kernel(SegMap m, int H, int dd, const float *init, const float *__r
         int64_t start, end;
         int base, count;
         if (!seq_segments(m, n, start, end, base, count)) continue;
+        if (count == 1) continue;                      // starts from init itself
         float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
         if (init != nullptr)
             S = *reinterpret_cast<const float4 *>(init + ((size_t)n * H + h) * dd + e);
         const int step = kReverse ? -1 : 1;
         int u = kReverse ? base + count - 1 : base;
         // the last segment in scan order has no R: nothing starts from its end
-        float4 next = S;
-        if (count > 1) next = *reinterpret_cast<const float4 *>(ws + ((size_t)u * H + h) * dd + e);
+        float4 next = *reinterpret_cast<const float4 *>(ws + ((size_t)u * H + h) * dd + e);
         for (int i = 0; i < count; ++i, u += step) {
             const float4 R = next;
             if (i + 2 < count)

@@ -176,7 +176,7 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
     if (u == 0 && h == 0 && c0 == 0) check_seqlens(m);
     Segment sg;
     if (!find_segment(m, u, sg)) return;
-    const float *from = ws != nullptr ? ws + ((size_t)u * H + h) * D * D
+    const float *from = ws != nullptr && sg.count > 1 ? ws + ((size_t)u * H + h) * D * D
                         : h0 != nullptr ? h0 + ((size_t)sg.n * H + h) * D * D : nullptr;
     Tile<D, W> S;
 #pragma unroll
@@ -311,7 +311,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     Segment sg;
     if (!find_segment(m, u, sg)) return;
     const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
-    const float *from = wsS != nullptr ? wsS + seg : h0 != nullptr ? h0 + seq : nullptr;
+    const float *from = wsS != nullptr && sg.count > 1 ? wsS + seg : h0 != nullptr ? h0 + seq : nullptr;
     Tile<D, D> S;
 #pragma unroll
     for (int i = 0; i < S.kI; ++i)
@@ -371,7 +371,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 #pragma unroll
             for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (D + 1) + S.n(j)] = S.v[i][j];
     }
-    const float *to = wsE != nullptr ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
+    const float *to = wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
     double s = 0.0;
     if (to != nullptr)
 #pragma unroll
@@ -409,7 +409,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
         return;
     }
     const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
-    const float *from = wsE != nullptr ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
+    const float *from = wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
     Tile<D, D> E;
 #pragma unroll
     for (int i = 0; i < E.kI; ++i)
