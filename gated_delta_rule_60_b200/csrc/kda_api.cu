@@ -15,6 +15,7 @@
 #include "kda_linear_simt.cuh"
 #include "kda_linear_decode.cuh"
 #include "kda_linear_sm100.cuh"
+#include "kda_linear_mma.cuh"
 #include "kda_rotary.cuh"
 #include "kda_layernorm.cuh"
 

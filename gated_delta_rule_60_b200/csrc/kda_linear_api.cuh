@@ -9,18 +9,42 @@ constexpr int64_t kNoSplit = int64_t(1) << 40;         // segment length of "one
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Tokens of a segment.  With chains = (sequence, head, column block) triples,
-// no split is made when they fill the GPU and their lengths are known to be
-// equal; else a segment is a quarter of an SM's even share of the tokens, so
-// that no long sequence is left over at the end.
-inline int64_t segment_length(int32_t N, bool equal, int64_t T_tot, int64_t chains_per_seq, int chunk) {
-    const int64_t kSMs = 148;
+// What a plan is made for: how many blocks run at once, and about what a chunk of
+// `tok` tokens costs a block in the main passes and in those that form the segments'
+// states (microseconds on a B200; only their ratios and the 8 us of two further
+// launches matter).
+struct Costs {
+    int tok, slots;
+    double main_us, state_us;
+};
+
+// Tokens of a segment, for `chains` blocks per sequence.  Equal lengths: the number
+// of segments that minimises the waves of both passes (the first over all segments
+// but the last).  Lengths that the host does not know: a slot's even share of the
+// tokens, which bounds what one long sequence can leave over; sequences below it
+// stay whole.  16 x 131,072 tokens: 9 segments 0.86 ms, unsplit 3.9 ms; 96 x 8,192:
+// unsplit 0.28 ms, any split adds a pass over all but the last segment.
+inline int64_t segment_length(int32_t N, bool equal, int64_t T_tot, int64_t chains, const Costs &c) {
     if (N <= 0 || T_tot <= 0) return kNoSplit;
-    if ((equal || N == 1) && N * chains_per_seq >= 2 * kSMs) return kNoSplit;
-    int64_t L = (T_tot * chains_per_seq + 4 * kSMs - 1) / (4 * kSMs);
-    if (L < 256) L = 256;
-    L = (L + chunk - 1) / chunk * chunk;
-    return L >= T_tot ? kNoSplit : L;
+    if (!equal && N > 1) {
+        int64_t L = (T_tot * chains + c.slots - 1) / c.slots;
+        if (L < 8 * c.tok) L = 8 * c.tok;
+        L = (L + c.tok - 1) / c.tok * c.tok;
+        return L >= T_tot ? kNoSplit : L;
+    }
+    const int64_t len = (T_tot + N - 1) / N, chunks = (len + c.tok - 1) / c.tok;
+    auto waves = [&](int64_t blocks) { return (double)((blocks + c.slots - 1) / c.slots); };
+    double best = waves(N * chains) * c.main_us * (double)chunks;
+    int64_t L = kNoSplit;
+    for (int64_t G = 2; G <= 64 && G * 4 <= chunks; ++G) {
+        const int64_t per = (chunks + G - 1) / G;
+        const double t = (double)per * (waves(N * chains * G) * c.main_us + waves(N * chains * (G - 1)) * c.state_us) + 8.0;
+        if (t < best) {
+            best = t;
+            L = per * c.tok;
+        }
+    }
+    return L;
 }
 
 struct Plan {
@@ -43,50 +67,32 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
     return p;
 }
 
-// The tensor-core kernels: one block an SM, a chunk of 128 tokens takes about
-// 1.7 us there, and 0.9 us where only states are wanted.
+// bf16 at d = 128 runs on tcgen05 (prefill), other bf16 on warp-level matrix
+// instructions, fp32 on CUDA cores.
 inline bool tensor_path(int32_t d, kda_dtype dt) { return d == 128 && dt == KDA_BF16; }
 
-// Equal lengths: the number of segments that minimises the waves of both passes
-// (the first over all segments but the last) and the two further launches.
-// Lengths that the host does not know: an SM's even share of the tokens, which
-// bounds what one long sequence can leave over.
-inline int64_t tensor_length(int32_t N, bool equal, int64_t T_tot, int32_t H) {
-    const int64_t kSMs = 148;
-    if (N <= 0 || T_tot <= 0) return kNoSplit;
-    if (!equal) {
-        int64_t L = (T_tot * H + kSMs - 1) / kSMs;
-        if (L < 1024) L = 1024;
-        L = (L + tc::kTok - 1) / tc::kTok * tc::kTok;
-        return L >= T_tot ? kNoSplit : L;
-    }
-    const int64_t len = (T_tot + N - 1) / N, chunks = (len + tc::kTok - 1) / tc::kTok;
-    auto waves = [&](int64_t blocks) { return (double)((blocks + kSMs - 1) / kSMs); };
-    double best = waves((int64_t)N * H) * 1.7 * (double)chunks;
-    int64_t L = kNoSplit;
-    for (int64_t G = 2; G <= 64 && G * 4 <= chunks; ++G) {
-        const int64_t per = (chunks + G - 1) / G;
-        const double t = ((double)per) * (waves((int64_t)N * H * G) * 1.7 + waves((int64_t)N * H * (G - 1)) * 0.9) + 8.0;
-        if (t < best) {
-            best = t;
-            L = per * tc::kTok;
-        }
-    }
-    return L;
+inline Costs fwd_costs(int32_t d, kda_dtype dt) {
+    if (tensor_path(d, dt)) return {tc::kTok, 148, 1.9, 1.0};
+    if (dt == KDA_BF16) return {mm::kTok, 148 * (d == 64 ? 3 : 6), d == 64 ? 2.5 : 1.5, d == 64 ? 1.2 : 0.8};
+    return {kC, 148 * (d >= 64 ? 2 : 4), 4.0, 1.5};
+}
+
+inline Costs bwd_costs(int32_t d, kda_dtype dt) {
+    if (dt == KDA_BF16)
+        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 9.0 : 4.0, d == 128 ? 3.4 : 1.6};
+    return {kC, 148 * (d == 128 ? 1 : 2), d == 128 ? 16.0 : 8.0, d == 128 ? 6.0 : 3.0};
 }
 
 // The workspace query does not know whether cu_seqlens is given: with several
 // sequences it takes the larger of the two plans.
 inline int64_t fwd_length(int32_t N, bool equal, int64_t T_tot, int32_t H, int32_t d, kda_dtype dt) {
-    return tensor_path(d, dt) ? tensor_length(N, equal || N == 1, T_tot, H)
-                              : segment_length(N, false, T_tot, (int64_t)H * (d < 64 ? 1 : d / 64), kC);
+    return segment_length(N, equal, T_tot, (int64_t)H * (dt == KDA_FP32 && d == 128 ? 2 : 1), fwd_costs(d, dt));
 }
 
 inline size_t fwd_bytes(const Plan &p) { return p.state_bytes + p.total_bytes; }
 
-inline int64_t bwd_length(int32_t N, int64_t T_tot, int32_t H, int32_t d) {
-    (void)d;
-    return segment_length(N, false, T_tot, H, kC);
+inline int64_t bwd_length(int32_t N, bool equal, int64_t T_tot, int32_t H, int32_t d, kda_dtype dt) {
+    return segment_length(N, equal, T_tot, H, bwd_costs(d, dt));
 }
 
 struct BwdSizes {
@@ -172,28 +178,53 @@ struct FwdArgs {
     unsigned char *ws;
 };
 
-template <typename T, int D>
+template <int D>
 kda_status fwd_simt(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     float *states = nullptr, *total = nullptr;
     const dim3 grid((unsigned)p.map.units, (unsigned)a.H, (unsigned)(D / OutSmem<D>::kW));
+    const float *q = (const float *)a.q, *k = (const float *)a.k, *v = (const float *)a.v;
     if (p.split) {
         states = reinterpret_cast<float *>(a.ws);
         total = reinterpret_cast<float *>(a.ws + p.state_bytes);
-        auto kern = state_kernel<T, D, false>;
+        auto kern = state_kernel<float, D, false>;
         const size_t smem = sizeof(StateSmem<D>);
         if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-        kern<<<grid, kThreads, smem, s>>>((const T *)a.k, (const T *)a.v, a.g, a.per_token, p.map,
-                                          a.Hk, a.H, 1.f, states, total);
+        kern<<<grid, kThreads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, states, total);
         kda_status st = launched();
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, total, states, s);
         if (st != KDA_OK) return st;
     }
-    auto kern = out_kernel<T, D>;
+    auto kern = out_kernel<float, D>;
     const size_t smem = sizeof(OutSmem<D>);
     if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-    kern<<<grid, kThreads, smem, s>>>((const T *)a.q, (const T *)a.k, (const T *)a.v, a.g,
-                                      a.per_token, a.h0, p.map, a.Hk, a.H, a.scale, states,
-                                      (T *)a.o, a.hT);
+    kern<<<grid, kThreads, smem, s>>>(q, k, v, a.g, a.per_token, a.h0, p.map, a.Hk, a.H, a.scale, states,
+                                      (float *)a.o, a.hT);
+    return launched();
+}
+
+// bf16 below d = 128
+template <int D>
+kda_status fwd_mma(const Plan &p, const FwdArgs &a, cudaStream_t s) {
+    float *states = nullptr, *total = nullptr;
+    const unsigned blocks = (unsigned)((int64_t)p.map.units * a.H), threads = mm::Shape<D>::kThreads;
+    const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q, *k = (const __nv_bfloat16 *)a.k,
+                        *v = (const __nv_bfloat16 *)a.v;
+    if (p.split) {
+        states = reinterpret_cast<float *>(a.ws);
+        total = reinterpret_cast<float *>(a.ws + p.state_bytes);
+        auto kern = mm::state_kernel<D, false>;
+        const size_t smem = sizeof(mm::StateSmem<D>);
+        if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
+        kern<<<blocks, threads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, states, total);
+        kda_status st = launched();
+        if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, total, states, s);
+        if (st != KDA_OK) return st;
+    }
+    auto kern = mm::out_kernel<D>;
+    const size_t smem = sizeof(mm::OutSmem<D>);
+    if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
+    kern<<<blocks, threads, smem, s>>>(q, k, v, a.g, a.per_token, a.h0, p.map, a.Hk, a.H, a.scale, states,
+                                       (__nv_bfloat16 *)a.o, a.hT);
     return launched();
 }
 
@@ -256,63 +287,80 @@ kda_status launch_group_sum(const float *part, void *out, int64_t T_tot, int32_t
     return launched();
 }
 
-template <typename T, int D>
-kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
-    const BwdSizes z = bwd_sizes(p, p.map.T_tot, a.Hk, a.H, D);
-    unsigned char *w = a.ws;
-    float *wsS = p.split ? (float *)w : nullptr;
-    w += z.states;
-    float *wsE = p.split ? (float *)w : nullptr;
-    w += z.states;
-    float *totS = (float *)w;
-    w += z.totals;
-    float *totE = (float *)w;
-    w += z.totals;
-    float *term = (float *)w;
-    w += z.terms;
-    double *anchor = (double *)w;
-    w += z.anchors;
-    double *sums = (double *)w;
-    w += z.sums;
-    float *part = z.parts ? (float *)w : nullptr;
+// Where a gradient call's workspace has what.
+struct BwdSpace {
+    float *S, *E, *totS, *totE, *term, *part;
+    double *anchor, *sums;
+};
+
+inline BwdSpace bwd_space(const Plan &p, const BwdSizes &z, unsigned char *w) {
+    BwdSpace b;
+    auto take = [&](size_t n) {
+        unsigned char *at = w;
+        w += n;
+        return at;
+    };
+    b.S = p.split ? (float *)take(z.states) : nullptr;
+    b.E = p.split ? (float *)take(z.states) : nullptr;
+    b.totS = (float *)take(z.totals);
+    b.totE = (float *)take(z.totals);
+    b.term = (float *)take(z.terms);
+    b.anchor = (double *)take(z.anchors);
+    b.sums = (double *)take(z.sums);
+    b.part = z.parts ? (float *)w : nullptr;
+    return b;
+}
+
+// The launches of a gradient: states of both directions and their scans when the
+// sequences are split, dQ, then dK and dV; shared heads' parts are added after each.
+template <typename T, int D, typename FS, typename RS, typename KQ, typename KKV>
+kda_status launch_bwd(const Plan &p, const BwdArgs &a, FS fs, RS rs, size_t state_smem, dim3 state_grid, KQ kq,
+                      size_t q_smem, KKV kkv, size_t kv_smem, dim3 grid, unsigned threads, cudaStream_t s) {
+    const BwdSpace b = bwd_space(p, bwd_sizes(p, p.map.T_tot, a.Hk, a.H, D), a.ws);
+    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dO = (const T *)a.dO;
     kda_status st = KDA_OK;
     if (p.split) {
-        const dim3 grid((unsigned)p.map.units, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
-        const size_t smem = sizeof(StateSmem<D>);
-        auto f = state_kernel<T, D, false>;
-        auto r = state_kernel<T, D, true>;
-        if (!set_smem(f, smem) || !set_smem(r, smem)) return KDA_ERR_CUDA;
-        f<<<grid, kThreads, smem, s>>>((const T *)a.k, (const T *)a.v, a.g, a.per_token, p.map,
-                                       a.Hk, a.H, 1.f, wsS, totS);
-        r<<<grid, kThreads, smem, s>>>((const T *)a.q, (const T *)a.dO, a.g, a.per_token, p.map,
-                                       a.Hk, a.H, a.scale, wsE, totE);
+        if (!set_smem(fs, state_smem) || !set_smem(rs, state_smem)) return KDA_ERR_CUDA;
+        fs<<<state_grid, threads, state_smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, b.S, b.totS);
+        rs<<<state_grid, threads, state_smem, s>>>(q, dO, a.g, a.per_token, p.map, a.Hk, a.H, a.scale, b.E, b.totE);
         st = launched();
-        if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, totS, wsS, s);
-        if (st == KDA_OK) st = launch_scan<true>(p, a.H, D, a.dhT, totE, wsE, s);
+        if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, b.totS, b.S, s);
+        if (st == KDA_OK) st = launch_scan<true>(p, a.H, D, a.dhT, b.totE, b.E, s);
         if (st != KDA_OK) return st;
     }
-    const dim3 grid((unsigned)p.map.units, (unsigned)a.H);
-    const size_t smem = sizeof(GradSmem<D>);
-    auto kq = grad_q_kernel<T, D>;
-    auto kkv = grad_kv_kernel<T, D>;
-    if (!set_smem(kq, smem) || !set_smem(kkv, smem)) return KDA_ERR_CUDA;
-    kq<<<grid, kThreads, smem, s>>>((const T *)a.q, (const T *)a.k, (const T *)a.v,
-                                    (const T *)a.dO, a.g, a.per_token, a.h0, a.dhT, p.map, a.Hk,
-                                    a.H, a.scale, wsS, wsE, (T *)a.dq, part, term, anchor);
+    if (!set_smem(kq, q_smem) || !set_smem(kkv, kv_smem)) return KDA_ERR_CUDA;
+    kq<<<grid, threads, q_smem, s>>>(q, k, v, dO, a.g, a.per_token, a.h0, a.dhT, p.map, a.Hk, a.H, a.scale, b.S,
+                                     b.E, (T *)a.dq, b.part, b.term, b.anchor);
     st = launched();
-    if (st == KDA_OK && part) st = launch_group_sum<T>(part, a.dq, p.map.T_tot, a.Hk, a.H, D, s);
+    if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dq, p.map.T_tot, a.Hk, a.H, D, s);
     if (st != KDA_OK) return st;
-    kkv<<<grid, kThreads, smem, s>>>((const T *)a.q, (const T *)a.k, (const T *)a.v,
-                                     (const T *)a.dO, a.g, a.per_token, a.dhT, p.map, a.Hk, a.H,
-                                     a.scale, wsE, term, anchor, (T *)a.dk, part, (T *)a.dv, a.dg,
-                                     sums, a.dh0);
+    kkv<<<grid, threads, kv_smem, s>>>(q, k, v, dO, a.g, a.per_token, a.dhT, p.map, a.Hk, a.H, a.scale, b.E,
+                                       b.term, b.anchor, (T *)a.dk, b.part, (T *)a.dv, a.dg, b.sums, a.dh0);
     st = launched();
-    if (st == KDA_OK && part) st = launch_group_sum<T>(part, a.dk, p.map.T_tot, a.Hk, a.H, D, s);
+    if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dk, p.map.T_tot, a.Hk, a.H, D, s);
     if (st == KDA_OK && !a.per_token) {
-        head_sum_kernel<<<(unsigned)a.H, kThreads, 0, s>>>(sums, a.dg, p.map.units, a.H);
+        head_sum_kernel<<<(unsigned)a.H, kThreads, 0, s>>>(b.sums, a.dg, p.map.units, a.H);
         st = launched();
     }
     return st;
+}
+
+template <int D>
+kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
+    const dim3 states((unsigned)p.map.units, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
+    return launch_bwd<float, D>(p, a, state_kernel<float, D, false>, state_kernel<float, D, true>,
+                                sizeof(StateSmem<D>), states, grad_q_kernel<float, D>, sizeof(GradSmem<D>),
+                                grad_kv_kernel<float, D>, sizeof(GradSmem<D>),
+                                dim3((unsigned)p.map.units, (unsigned)a.H), kThreads, s);
+}
+
+template <int D>
+kda_status bwd_mma(const Plan &p, const BwdArgs &a, cudaStream_t s) {
+    const dim3 grid((unsigned)((int64_t)p.map.units * a.H));
+    return launch_bwd<__nv_bfloat16, D>(p, a, mm::state_kernel<D, false>, mm::state_kernel<D, true>,
+                                        sizeof(mm::StateSmem<D>), grid, mm::grad_q_kernel<D>,
+                                        sizeof(mm::GradSmem<D>), mm::grad_kv_kernel<D>,
+                                        sizeof(mm::GradKvSmem<D>), grid, mm::Shape<D>::kThreads, s);
 }
 
 template <typename T, int D>
@@ -325,17 +373,32 @@ kda_status step(const void *q, const void *k, const void *v, const float *g, int
     return launched();
 }
 
-// f<T, D>(...) by the run-time type and head size.
-#define KDA_LIN_DISPATCH(f, dt, d, ...)                                                     \
-    ((dt) == KDA_BF16                                                                       \
-         ? ((d) == 16   ? f<__nv_bfloat16, 16>(__VA_ARGS__)                                 \
-            : (d) == 32 ? f<__nv_bfloat16, 32>(__VA_ARGS__)                                 \
-            : (d) == 64 ? f<__nv_bfloat16, 64>(__VA_ARGS__)                                 \
-                        : f<__nv_bfloat16, 128>(__VA_ARGS__))                               \
-         : ((d) == 16   ? f<float, 16>(__VA_ARGS__)                                         \
-            : (d) == 32 ? f<float, 32>(__VA_ARGS__)                                         \
-            : (d) == 64 ? f<float, 64>(__VA_ARGS__)                                         \
-                        : f<float, 128>(__VA_ARGS__)))
+// f<D>(...) by the run-time head size.
+#define KDA_LIN_BY_D(f, d, ...)            \
+    ((d) == 16   ? f<16>(__VA_ARGS__)      \
+     : (d) == 32 ? f<32>(__VA_ARGS__)      \
+     : (d) == 64 ? f<64>(__VA_ARGS__)      \
+                 : f<128>(__VA_ARGS__))
+
+inline kda_status fwd(int d, kda_dtype dt, const Plan &p, const FwdArgs &a, cudaStream_t s) {
+    if (dt == KDA_FP32) return KDA_LIN_BY_D(fwd_simt, d, p, a, s);
+    return d == 16   ? fwd_mma<16>(p, a, s)
+           : d == 32 ? fwd_mma<32>(p, a, s)
+           : d == 64 ? fwd_mma<64>(p, a, s)
+                     : fwd_tensor(p, a, s);
+}
+
+inline kda_status bwd(int d, kda_dtype dt, const Plan &p, const BwdArgs &a, cudaStream_t s) {
+    if (dt == KDA_FP32) return KDA_LIN_BY_D(bwd_simt, d, p, a, s);
+    return KDA_LIN_BY_D(bwd_mma, d, p, a, s);
+}
+
+template <int D>
+kda_status step_any(kda_dtype dt, const void *q, const void *k, const void *v, const float *g, int per_token,
+                    float *S, void *o, int64_t units, int Hk, int H, float scale, cudaStream_t s) {
+    return dt == KDA_BF16 ? step<__nv_bfloat16, D>(q, k, v, g, per_token, S, o, units, Hk, H, scale, s)
+                          : step<float, D>(q, k, v, g, per_token, S, o, units, Hk, H, scale, s);
+}
 
 }  // namespace lin
 }  // namespace kda
@@ -374,8 +437,7 @@ extern "C" KDA_API kda_status kda_linear_chunk_fwd(
     const kda::lin::FwdArgs a = {q, k, v, g, h0, g_per_token, Hk, H, scale, o, hT,
                                  (unsigned char *)workspace};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (kda::lin::tensor_path(d, dt)) return kda::lin::fwd_tensor(p, a, s);
-    return KDA_LIN_DISPATCH(kda::lin::fwd_simt, dt, d, p, a, s);
+    return kda::lin::fwd(d, dt, p, a, s);
 }
 
 extern "C" KDA_API kda_status kda_linear_decode_step(
@@ -390,18 +452,23 @@ extern "C" KDA_API kda_status kda_linear_decode_step(
     if ((int64_t)B * H > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
     const void *req[] = {q, k, v, S, o};
     if (!kda::lin::all_given(req, 5) || !kda::lin::given4(g)) return KDA_ERR_INVALID_ARGUMENT;
-    return KDA_LIN_DISPATCH(kda::lin::step, dt, d, q, k, v, g, g_per_token, S, o, (int64_t)B * H,
-                            Hk, H, scale, reinterpret_cast<cudaStream_t>(stream));
+    return KDA_LIN_BY_D(kda::lin::step_any, d, dt, q, k, v, g, g_per_token, S, o, (int64_t)B * H, Hk,
+                        H, scale, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" KDA_API size_t kda_linear_chunk_bwd_workspace_size(int32_t N, int64_t T_tot,
                                                               int32_t Hk, int32_t H, int32_t d,
                                                               kda_dtype dt) {
-    if (N <= 0 || T_tot < 0 || H <= 0 || Hk <= 0 || !kda::lin::supported_d(d)) return 0;
+    using namespace kda::lin;
+    if (N <= 0 || T_tot < 0 || H <= 0 || Hk <= 0 || !supported_d(d)) return 0;
     if (dt != KDA_BF16 && dt != KDA_FP32) return 0;
-    const kda::lin::Plan p = kda::lin::make_plan(nullptr, N, T_tot, H, d,
-                                                 kda::lin::bwd_length(N, T_tot, H, d));
-    return kda::lin::bwd_sizes(p, T_tot, Hk, H, d).all;
+    size_t most = 0;
+    for (int equal = 0; equal < 2; ++equal) {
+        const Plan p = make_plan(nullptr, N, T_tot, H, d, bwd_length(N, equal, T_tot, H, d, dt));
+        const size_t n = bwd_sizes(p, T_tot, Hk, H, d).all;
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 extern "C" KDA_API kda_status kda_linear_chunk_bwd(
@@ -427,13 +494,15 @@ extern "C" KDA_API kda_status kda_linear_chunk_bwd(
         return KDA_ERR_INVALID_ARGUMENT;
     if (!kda::lin::ok16(h0) || !kda::lin::ok16(dhT) || !kda::lin::ok16(dh0))
         return KDA_ERR_INVALID_ARGUMENT;
-    const kda::lin::Plan p = kda::lin::make_plan(cu_seqlens, N, T_tot, H, d,
-                                                 kda::lin::bwd_length(N, T_tot, H, d));
-    const size_t need = kda::lin::bwd_sizes(p, T_tot, Hk, H, d).all;
+    const kda::lin::Plan p = kda::lin::make_plan(
+        cu_seqlens, N, T_tot, H, d,
+        kda::lin::bwd_length(N, cu_seqlens == nullptr, T_tot, H, d, dt));
+    if ((int64_t)p.map.units * H > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
+    const size_t need = kda_linear_chunk_bwd_workspace_size(N, T_tot, Hk, H, d, dt);
     if (workspace == nullptr || workspace_bytes < need ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return KDA_ERR_WORKSPACE;
     const kda::lin::BwdArgs a = {q, k, v, dO, g, h0, dhT, g_per_token, Hk, H, scale,
                                  dq, dk, dv, dg, dh0, (unsigned char *)workspace};
-    return KDA_LIN_DISPATCH(kda::lin::bwd_simt, dt, d, p, a, s);
+    return kda::lin::bwd(d, dt, p, a, s);
 }

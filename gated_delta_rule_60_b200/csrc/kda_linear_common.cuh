@@ -22,6 +22,7 @@
 #pragma once
 
 #include "kda_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace kda {
 namespace lin {
@@ -109,6 +110,51 @@ __device__ __forceinline__ double warp_scan(double x) {
         if (lane >= o) x += y;
     }
     return x;
+}
+
+// A decay sum as two floats, hi the nearest to the whole: 48 bits, as differences of
+// sums behind a strong decay need (fp64 arithmetic would do, at several times the
+// latency, where a warp forms the factors that others wait for).
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 add2(Sum2 a, Sum2 b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+    const float r = s + e;
+    return {r, e - (r - s)};
+}
+__device__ __forceinline__ Sum2 minus(Sum2 a) { return {-a.hi, -a.lo}; }
+// e^t without the rounding of t
+__device__ __forceinline__ float exp_sum(Sum2 t) {
+    const float e = expf(t.hi);
+    return fmaf(e, t.lo, e);
+}
+
+__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// x = hi + mid + lo in bf16 pairs, each the leading 8 bits of what is left: cut,
+// not rounded, so that a part costs a byte permute instead of a conversion.  What
+// is left over is below 2^-24 of x.
+__device__ __forceinline__ float2 cut_bf16(float2 x) {
+    return make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                                 __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_cut(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+__device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    const float2 minus = make_float2(-1.f, -1.f);
+    hi = pack_cut(x);
+    x = sm100::ffma2(cut_bf16(x), minus, x);
+    mid = pack_cut(x);
+    x = sm100::ffma2(cut_bf16(x), minus, x);
+    lo = pack_cut(x);
 }
 
 // Scan over the segments of one (sequence, head): on entry ws[u][h] holds the

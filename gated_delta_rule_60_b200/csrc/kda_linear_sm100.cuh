@@ -11,9 +11,12 @@
 // so both products of O share one accumulator and the decay costs one multiply
 // per element of P' and one per element of O.  The level is the middle of the
 // extremes, and a chunk whose b stays within 60 of it keeps every factor inside
-// e^{+-60}, far inside the range of bf16 and fp32.  A chunk that decays further
-// takes the slow form: P'_ij e^{b_i - b_j} by an exponential of its own, the rows
-// of Q scaled by e^{b_i} in place, m = 0.
+// e^{+-60}, far inside the range of bf16 and fp32.  A chunk that decays by more
+// than e^{-120} takes a level for each 32 tokens, all of them powers of two:
+// P'_ij gains the ratio of its row's level to its column's, and the rows of Q are
+// scaled in place by the ratio of theirs to the first (exact).  Where 32 tokens
+// decay by more than e^{-120}, every row takes a level, m = 0 for S'', and P'_ij an
+// exponential of its own.
 //
 // Precision.  O rounds P' and S'' to bf16 once each (2^-8 of a term); its sum and
 // the row factor are fp32.  S is fp32 in registers and must not take a bf16
@@ -55,21 +58,25 @@ constexpr uint32_t kColX = 0, kColP = 128, kColD = 192, kColV = 320, kVBuf = 96,
 constexpr float kRange = 60.f;                         // |b - m| of the fast form
 constexpr unsigned long long kWaitLimit = 4000000000ull;   // about 2 s of SM clock
 
+// How the decay of a chunk is split into factors (b, m of the comment above).
+enum : int { kOneLevel = 0, kFourLevels = 1, kDirect = 2 };
+
 struct __align__(16) Decay {
-    float x[kTok], y[kTok];    // fast: e^{m - b}, r;  slow: b as a sum of two floats
-    float kv;                  // fast: e^{b_C - m}
-    float em;                  // e^m (slow: 1)
+    float x[kTok], y[kTok];    // e^{m - b}, r;  direct: b as a sum of two floats
+    float kv[4];               // e^{b_C - m} for the m of 32 tokens
+    int level[4];              // m = level ln 2
+    float em;                  // e^m of the first (direct: 1)
     float gamma;               // e^{b_C}
-    float end_hi, end_lo;      // slow: b_C
-    int slow;
+    float end_hi, end_lo;      // direct: b_C
+    int mode;
 };
 
 struct Small {
     Decay dec[kStages];
-    uint64_t full[kStages], dec_full[kStages], dec_free[kStages];
+    uint64_t full[kStages], dec_free[kStages];
     uint64_t staged[kStages], k_free[kStages];
-    uint64_t d1_full, p_ready, o_full, x_free, s_ready;
-    uint64_t v_full[2], v_free[2], ds_full, ds_free;
+    uint64_t d1_full, p_ready, o_full, x_free;
+    uint64_t v_full[2], v_free, ds_full, ds_free;
     uint64_t drain[2];
     uint32_t tmem;
     volatile int abort;
@@ -84,14 +91,21 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// A wait that every lane polls; false after the limit, or once another role gave up.
+// A wait that every lane polls (each poll may suspend the warp for up to 10 us);
+// false once another role gave up, or after kPolls polls: 2 s at most, and 4 ms
+// at least where a poll returns at once.  The loop is kept short: sixteen warps
+// in six roles share the instruction caches.
+constexpr int kPolls = 1 << 18;
 __device__ __forceinline__ bool wait(Small &sm, uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &sm.abort, kWaitLimit));
-    if (!ok) {
-        if (!sm.abort) raise_error(kErrTimeout);
-        sm.abort = 1;
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+#pragma unroll 1
+    for (int n = 0; n < kPolls; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, 10000))) return true;
+        if (sm.abort) return false;
     }
-    return ok;
+    raise_error(kErrTimeout);
+    sm.abort = 1;
+    return false;
 }
 
 // One arrival of a warp, after all of its lanes.
@@ -100,30 +114,79 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// tcgen05.st 16 lanes x 128 bits, four times: 16 columns.  Register 2 c + r holds
-// row lane / 4 + 8 r, column 4 c + lane % 4: the fragments of ldmatrix.
-__device__ __forceinline__ void tmem_st_frag(uint32_t addr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// tcgen05.st 16 lanes x 128 bits, twice: 8 columns.  Register 2 c + r holds row
+// lane / 4 + 8 r, column 4 c + lane % 4: the fragments of ldmatrix.
+__device__ __forceinline__ void tmem_st_frag(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
 
-__device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+// level ln 2, in two parts: the first has 10 bits, and what its product with a
+// large level does not hold is kept too.
+__device__ __forceinline__ Sum2 level_sum(int level) {
+    const float l = (float)level, hi = l * 0.693359375f;
+    return add2({hi, fmaf(l, 0.693359375f, -hi)}, {l * -2.12194440054690583e-4f, 0.f});
 }
 
-// x = hi + mid + lo in bf16 pairs; what is left is below 2^-24 of x.
-__device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    hi = pack_bf16(x.x, x.y);
-    float2 h = bf16x2_to_float2(hi);
-    x = fadd2(x, make_float2(-h.x, -h.y));
-    mid = pack_bf16(x.x, x.y);
-    h = bf16x2_to_float2(mid);
-    x = fadd2(x, make_float2(-h.x, -h.y));
-    lo = pack_bf16(x.x, x.y);
+// Direct form: every row has a level of its own.
+__device__ __forceinline__ int row_level(const Decay &d, int row) {
+    const float l = rintf(d.x[row] * kLog2e);
+    return l < -4e6f ? -4000000 : (int)l;
+}
+__device__ __noinline__ float direct_row_factor(const Decay &d, int row, float scale) {
+    return scale * exp_sum(add2({d.x[row], d.y[row]}, minus(level_sum(row_level(d, row)))));
+}
+
+// One 32 x 32 block of P' in the direct form, an exponential for every element.
+__device__ __noinline__ void direct_block(const Decay &d, uint32_t from, uint32_t to, int row, int j0) {
+    const Sum2 m = level_sum(row_level(d, row));
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8, from += 8, to += 4) {
+        uint32_t r[8], o[4];
+        prefill::tmem_ld8(from, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + c + i;
+            const float x = __uint_as_float(r[i]) * __expf((m.hi - d.x[j]) + (m.lo - d.y[j]));
+            r[i] = __float_as_uint(row >= j ? x : 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(o[0]),
+                     "r"(o[1]), "r"(o[2]), "r"(o[3])
+                     : "memory");
+    }
+}
+
+// Row `row` of a tile of 128 channels times a, in place.
+__device__ __noinline__ void scale_row(unsigned char *tile, int row, float a) {
+    const __nv_bfloat162 f = __float2bfloat162_rn(a);
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        uint4 *x = reinterpret_cast<uint4 *>(tile + (i >> 3) * kHalf + sw128_off(row, 8 * (i & 7)));
+        uint4 y = *x;
+        __nv_bfloat162 *yw = reinterpret_cast<__nv_bfloat162 *>(&y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) yw[j] = __hmul2(yw[j], f);
+        *x = y;
+    }
+}
+
+// Rows L .. of K and V (the tile behind it) are another sequence's, or nobody's:
+// zero times a NaN there would still be one.  By the 8 warps of S, who read V next
+// and publish S'' (which every product of V waits for) after it.
+__device__ __noinline__ void clear_tail(unsigned char *k, int L) {
+    const int t = threadIdx.x - 256, row = t >> 1;
+    if (row >= L)
+        for (int i = 0; i < 8; ++i) {
+            uint4 *x = reinterpret_cast<uint4 *>(k + (t & 1) * kHalf + sw128_off(row, 8 * i));
+            x[0] = make_uint4(0, 0, 0, 0);
+            x[kTile / sizeof(uint4)] = make_uint4(0, 0, 0, 0);
+        }
+    fence_proxy_async_smem();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
 struct Params {
@@ -137,48 +200,82 @@ struct Params {
     float scale;
 };
 
-// Decay factors of chunk tokens 4 lane .. 4 lane + 3 (warp 2); returns b_C.
-__device__ __forceinline__ double decay_factors(Decay &d, const float (&g)[4], float scale) {
+// Decay factors of chunk tokens 4 lane .. 4 lane + 3 (warp 2), formed before the
+// slot they go to is free.
+struct LaneDecay {
+    float x[4], y[4], kv, em, gamma;
+    Sum2 end;
+    int level, mode;
+};
+
+__device__ __forceinline__ void decay_factors(LaneDecay &d, const float (&g)[4], float scale) {
     const int lane = threadIdx.x & 31;
-    double b[4], run = 0.0;
+    Sum2 b[4];
+    b[0] = {g[0], 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = run += (double)g[i];
-    const double before = warp_scan(run) - run;
-    float top, low;
+    for (int i = 1; i < 4; ++i) b[i] = add2(b[i - 1], {g[i], 0.f});
+    Sum2 run = b[3], before = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] += before;
-    top = fmaxf(fmaxf((float)b[0], (float)b[1]), fmaxf((float)b[2], (float)b[3]));
-    low = fminf(fminf((float)b[0], (float)b[1]), fminf((float)b[2], (float)b[3]));
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum2 up = {__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
+        if (lane >= o) {
+            run = add2(up, run);
+            before = add2(up, before);
+        }
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < 4; ++i) b[i] = add2(before, b[i]);
+    d.end = {__shfl_sync(0xffffffffu, b[3].hi, 31), __shfl_sync(0xffffffffu, b[3].lo, 31)};
+    // extremes of 32 tokens (8 lanes), then of the chunk
+    float top = fmaxf(fmaxf(b[0].hi, b[1].hi), fmaxf(b[2].hi, b[3].hi));
+    float low = fminf(fminf(b[0].hi, b[1].hi), fminf(b[2].hi, b[3].hi));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
     }
-    const double end = __shfl_sync(0xffffffffu, b[3], 31);
-    const double m = 0.5 * ((double)top + (double)low);
-    const bool slow = !(top - low <= 2.f * kRange);    // NaN: slow
-    if (slow) {
+    const bool near32 = __all_sync(0xffffffffu, top - low <= 2.f * kRange);      // NaN: no
+    float top_c = top, low_c = low;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            d.x[4 * lane + i] = (float)b[i];
-            d.y[4 * lane + i] = (float)(b[i] - (double)(float)b[i]);
-        }
-    } else {
+    for (int o = 8; o < 32; o <<= 1) {
+        top_c = fmaxf(top_c, __shfl_xor_sync(0xffffffffu, top_c, o));
+        low_c = fminf(low_c, __shfl_xor_sync(0xffffffffu, low_c, o));
+    }
+    const bool near_c = top_c - low_c <= 2.f * kRange;
+    d.mode = near_c ? kOneLevel : near32 ? kFourLevels : kDirect;
+    if (near_c) {
+        top = top_c;
+        low = low_c;
+    }
+    const bool direct = d.mode == kDirect;
+    d.level = direct ? 0 : __float2int_rn(0.5f * (top + low) * kLog2e);
+    const Sum2 m = level_sum(d.level);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            d.x[4 * lane + i] = expf((float)(m - b[i]));
-            d.y[4 * lane + i] = scale * expf((float)(b[i] - m));
-        }
+    for (int i = 0; i < 4; ++i) {
+        const Sum2 t = add2(m, minus(b[i]));
+        d.x[i] = direct ? b[i].hi : exp_sum(t);
+        d.y[i] = direct ? b[i].lo : scale * exp_sum(minus(t));
+    }
+    d.kv = direct ? 1.f : exp_sum(add2(d.end, minus(m)));
+    d.em = direct ? 1.f : exp_sum(m);
+    d.gamma = exp_sum(d.end);
+}
+
+__device__ __forceinline__ void store_decay(Decay &o, const LaneDecay &d) {
+    const int lane = threadIdx.x & 31;
+    *reinterpret_cast<float4 *>(&o.x[4 * lane]) = make_float4(d.x[0], d.x[1], d.x[2], d.x[3]);
+    *reinterpret_cast<float4 *>(&o.y[4 * lane]) = make_float4(d.y[0], d.y[1], d.y[2], d.y[3]);
+    if ((lane & 7) == 0) {
+        o.kv[lane >> 3] = d.kv;
+        o.level[lane >> 3] = d.level;
     }
     if (lane == 0) {
-        d.kv = slow ? 1.f : expf((float)(end - m));
-        d.em = slow ? 1.f : expf((float)m);
-        d.gamma = expf((float)end);
-        d.end_hi = (float)end;
-        d.end_lo = (float)(end - (double)(float)end);
-        d.slow = slow;
+        o.em = d.em;
+        o.gamma = d.gamma;
+        o.end_hi = d.end.hi;
+        o.end_lo = d.end.lo;
+        o.mode = d.mode;
     }
-    return end;
 }
 
 // Longest first.  Blocks start in index order, so with the units of a batch in
@@ -222,24 +319,23 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     Segment sg;
     if (!find_segment(p.m, u, sg)) return;
     if (kStates && sg.s == sg.count - 1) return;
-    const int chunks = (int)((sg.t1 - sg.t0 + kTok - 1) / kTok);
+    const int len = (int)(sg.t1 - sg.t0);
+    const int chunks = (len + kTok - 1) / kTok;
     const int hk = h / (p.H / p.Hk);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.dec_full[i], 1);
+            mbar_init(&sm.full[i], 2);                 // the tiles, and the decay factors
             mbar_init(&sm.dec_free[i], kStates ? 8 : 12);
             mbar_init(&sm.staged[i], 4);
             mbar_init(&sm.k_free[i], 1);
             mbar_init(&sm.v_full[i], 8);
-            mbar_init(&sm.v_free[i], 1);
         }
+        mbar_init(&sm.v_free, 1);
         mbar_init(&sm.d1_full, 1);
-        mbar_init(&sm.p_ready, 4);
+        mbar_init(&sm.p_ready, 12);
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.x_free, 4);
-        mbar_init(&sm.s_ready, 8);
         mbar_init(&sm.ds_full, 1);
         mbar_init(&sm.ds_free, 8);
         mbar_init(&sm.drain[0], 1);
@@ -256,8 +352,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     tc_fence_after();
     const uint32_t tm = sm.tmem;
     const uint32_t base = smem_u32(sh);
-    auto rows_of = [&](int c) { return (int)(sg.t1 - sg.t0 - (int64_t)c * kTok < kTok
-                                                 ? sg.t1 - sg.t0 - (int64_t)c * kTok : kTok); };
+    const int t_first = (int)sg.t0;                    // tokens stay below 2^31
 
     if (warp == 0) {
         // ------------------------------------------------------------ tiles
@@ -265,7 +360,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             if (elect_one()) {
                 unsigned char *st = sh + (c & 1) * kStageBytes;
                 uint64_t *bar = &sm.full[c & 1];
-                const int t = (int)(sg.t0 + (int64_t)c * kTok);
+                const int t = t_first + c * kTok;
                 mbar_expect_tx(bar, kStates ? 2 * kTile : 3 * kTile);
                 tma_load_3d(st + kTile, &map_k, bar, 0, hk, t);
                 tma_load_3d(st + kTile + kHalf, &map_k, bar, 64, hk, t);
@@ -278,15 +373,30 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             }
             __syncwarp();
         };
+        // the tiles of the chunk after are brought to L2, so that a stage that becomes
+        // free is filled from there
+        auto prefetch = [&](int c) {
+            if (c < chunks && elect_one()) {
+                const int t = t_first + c * kTok;
+#pragma unroll
+                for (int x = 0; x < kD; x += 64) {
+                    tma_prefetch_3d(&map_k, x, hk, t);
+                    if (!kStates) tma_prefetch_3d(&map_q, x, hk, t);
+                    tma_prefetch_3d(&map_v, x, h, t);
+                }
+            }
+            __syncwarp();
+        };
         for (int c = 0; c < kStages && c < chunks; ++c) load(c);
+        prefetch(kStages);
         int c = 0;
         for (; c < chunks; ++c) {
             if (!kStates) {
                 if (!wait(sm, &sm.staged[c & 1], (c >> 1) & 1)) break;
-                if (rows_of(c) == kTok) {
+                if (len - c * kTok >= kTok) {
                     if (elect_one()) {
                         const unsigned char *st = sh + (c & 1) * kStageBytes;
-                        const int t = (int)(sg.t0 + (int64_t)c * kTok);
+                        const int t = t_first + c * kTok;
                         tma_store_3d(&map_o, st, 0, h, t);
                         tma_store_3d(&map_o, st + kHalf, 64, h, t);
                         bulk_commit_group();
@@ -297,6 +407,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             }
             if (!wait(sm, &sm.k_free[c & 1], (c >> 1) & 1)) break;
             if (c + kStages < chunks) load(c + kStages);
+            prefetch(c + kStages + 1);
         }
         if (c < chunks) {                              // gave up: let the copies in flight land
             const int issued = c + kStages < chunks ? c + kStages : chunks;
@@ -327,8 +438,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 tc_commit(&sm.d1_full);
             }
             __syncwarp();
-            if (!wait(sm, &sm.s_ready, c & 1)) break;
-            if (!wait(sm, &sm.p_ready, c & 1)) break;
+            if (!wait(sm, &sm.p_ready, c & 1)) break;  // P' and S''
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -349,21 +459,25 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         auto fetch = [&](int c, float (&x)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t t = sg.t0 + (int64_t)c * kTok + 4 * lane + i;
-                x[i] = t < sg.t1 ? load_decay(p.g, p.per_token, t, h, p.H) : 0.f;
+                const int t = c * kTok + 4 * lane + i;
+                x[i] = t < len ? load_decay(p.g, p.per_token, sg.t0 + t, h, p.H) : 0.f;
             }
         };
-        double sum = 0.0;
+        Sum2 sum = {0.f, 0.f};
         if (chunks > 0) fetch(0, next);
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) g[i] = next[i];
             if (c + 1 < chunks) fetch(c + 1, next);
+            LaneDecay d;
+            decay_factors(d, g, p.scale);
+            if (kStates) sum = add2(sum, d.end);
             if (c >= kStages && !wait(sm, &sm.dec_free[c & 1], ((c >> 1) - 1) & 1)) break;
-            sum += decay_factors(sm.dec[c & 1], g, p.scale);
-            arrive(&sm.dec_full[c & 1]);
+            store_decay(sm.dec[c & 1], d);
+            arrive(&sm.full[c & 1]);
         }
-        if (kStates && lane == 0) p.total[(size_t)u * p.H + h] = expf((float)sum);
+        if (kStates && lane == 0) p.total[(size_t)u * p.H + h] = exp_sum(sum);
     } else if (warp == 3) {
         // ------------------------------------------------------------ V'^T K
         constexpr uint32_t id = idesc_bf16(128, 128, false, true);
@@ -384,8 +498,9 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                         for (int k = 0; k < 4; ++k)
                             mma_ts(tm + kColD, tm + kColV + hf * kVBuf + part * kVPart + 8 * k,
                                    sdesc_at(dk, 2048 * (4 * hf + k)), id, hf > 0 || part < 2 || k > 0);
-                    tc_commit(&sm.v_free[hf]);
-                    if (hf == 1) {
+                    if (hf == 0) {
+                        tc_commit(&sm.v_free);
+                    } else {
                         tc_commit(&sm.ds_full);
                         tc_commit(&sm.k_free[c & 1]);
                     }
@@ -403,76 +518,61 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         for (int i = 0; i < 16; ++i) z[i] = 0u;
         for (int jb = w + 1; jb < 4; ++jb) tmem_st16(tq + kColP + 16 * jb, z);   // stays zero
         tmem_wait_st();
+        uint32_t below[16];                            // of a diagonal block: row >= column
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            below[i] = (lane >= 2 * i ? 0xffffu : 0u) | (lane >= 2 * i + 1 ? 0xffff0000u : 0u);
         for (int c = 0; c < chunks; ++c) {
             const Decay &d = sm.dec[c & 1];
             unsigned char *st = sh + (c & 1) * kStageBytes;
-            const int L = rows_of(c);
-            if (!wait(sm, &sm.dec_full[c & 1], (c >> 1) & 1)) break;
+            const bool whole_chunk = len - c * kTok >= kTok;
             if (!wait(sm, &sm.d1_full, c & 1)) break;
             tc_fence_after();
-            const bool slow = d.slow;
+            const int mode = d.mode;
+            const int level = d.level[w];
 #pragma unroll 1
             for (int jb = 0; jb <= w; ++jb) {
-                uint32_t r[32];
-                tmem_ld32(tq + kColX + 32 * jb, r);
-                float e[32];
-                if (!slow) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(&d.x[32 * jb + j]);
-                        e[j] = f.x; e[j + 1] = f.y; e[j + 2] = f.z; e[j + 3] = f.w;
-                    }
-                } else {
-                    const float hi = d.x[row], lo = d.y[row];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        e[j] = expf((hi - d.x[32 * jb + j]) + (lo - d.y[32 * jb + j]));
+                if (mode == kDirect) {
+                    direct_block(d, tq + kColX + 32 * jb, tq + kColP + 16 * jb, row, 32 * jb);
+                    continue;
                 }
+                uint32_t r[32], o[16];
+                tmem_ld32(tq + kColX + 32 * jb, r);
+                const uint32_t whole = jb < w ? 0xffffffffu : 0u;
+                const float ratio = exp2f((float)(level - d.level[jb]));   // 1 on one level
                 tmem_wait_ld();
-                uint32_t o[16];
+                if (mode == kFourLevels)
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    float2 x = fmul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
-                                     make_float2(e[j], e[j + 1]));
-                    if (jb == w) {
-                        x.x = lane >= j ? x.x : 0.f;
-                        x.y = lane >= j + 1 ? x.y : 0.f;
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 x = fmul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                               make_float2(ratio, ratio));
+                        r[j] = __float_as_uint(x.x);
+                        r[j + 1] = __float_as_uint(x.y);
                     }
-                    o[j / 2] = pack_bf16(x.x, x.y);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&d.x[32 * jb + j]);
+                    const float2 x = fmul2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])),
+                                           make_float2(f.x, f.y));
+                    const float2 y = fmul2(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])),
+                                           make_float2(f.z, f.w));
+                    o[j / 2] = pack_bf16(x.x, x.y) & (below[j / 2] | whole);
+                    o[j / 2 + 1] = pack_bf16(y.x, y.y) & (below[j / 2 + 1] | whole);
                 }
                 tmem_st16(tq + kColP + 16 * jb, o);
             }
-            if (slow) {                                // Q has been read by Q K^T
-                const float a = expf(d.x[row] + d.y[row]);
-#pragma unroll 1
-                for (int i = 0; i < 16; ++i) {
-                    uint4 *x = reinterpret_cast<uint4 *>(st + (i >> 3) * kHalf + sw128_off(row, 8 * (i & 7)));
-                    uint4 y = *x;
-                    uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = bf16x2_to_float2(yw[j]);
-                        yw[j] = pack_bf16(f.x * a, f.y * a);
-                    }
-                    *x = y;
-                }
-            }
-            if (row >= L) {                            // another sequence's values, never multiplied
-                unsigned char *v = st + 2 * kTile;
-#pragma unroll 1
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint4 *>(v + (i >> 3) * kHalf + sw128_off(row, 8 * (i & 7))) =
-                        make_uint4(0, 0, 0, 0);
-            }
-            if (slow || L < kTok) fence_proxy_async_smem();
+            // Q has been read by Q K^T
+            if (mode == kDirect) scale_row(st, row, exp2f((float)row_level(d, row)));
+            else if (level != d.level[0]) scale_row(st, row, exp2f((float)(level - d.level[0])));
+            if (mode != kOneLevel) fence_proxy_async_smem();
             tmem_wait_st();
             tc_fence_before();
             arrive(&sm.p_ready);
 
             if (!wait(sm, &sm.o_full, c & 1)) break;
             tc_fence_after();
-            const float a = slow ? p.scale : d.y[row];
-            __nv_bfloat16 *og = p.o + ((size_t)(sg.t0 + (int64_t)c * kTok + row) * p.H + h) * kD;
+            const float a = mode == kDirect ? direct_row_factor(d, row, p.scale) : d.y[row];
+            __nv_bfloat16 *og = p.o + ((size_t)(sg.t0 + c * kTok + row) * p.H + h) * kD;
 #pragma unroll 1
             for (int jb = 0; jb < 4; ++jb) {
                 uint32_t r[32];
@@ -494,10 +594,10 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                                                make_float2(a, a));
                         yw[i] = pack_bf16(x.x, x.y);
                     }
-                    if (L == kTok)
+                    if (whole_chunk)
                         *reinterpret_cast<uint4 *>(st + (jb >> 1) * kHalf +
                                                    sw128_off(row, 32 * (jb & 1) + 8 * j)) = y;
-                    else if (row < L)
+                    else if (c * kTok + row < len)
                         *reinterpret_cast<uint4 *>(og + 32 * jb + 8 * j) = y;
                 }
             }
@@ -522,63 +622,52 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         auto produce = [&](int c, int hf) -> bool {
             const Decay &d = sm.dec[c & 1];
             unsigned char *st = sh + (c & 1) * kStageBytes;
-            const int L = rows_of(c);
             if (hf == 0) {
                 if (!wait(sm, &sm.full[c & 1], (c >> 1) & 1)) return false;
-                if (!wait(sm, &sm.dec_full[c & 1], (c >> 1) & 1)) return false;
-                if (L < kTok) {                        // K rows of another sequence
-                    const int r = 8 * (warp - 8) * 2 + (lane >> 1);
-                    if (r >= L)
-#pragma unroll 1
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4 *>(st + kTile + (lane & 1) * kHalf + sw128_off(r, 8 * i)) =
-                                make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                }
+                if (len - c * kTok < kTok) clear_tail(st + kTile, len - c * kTok);
             }
-            if (c > 0 && !wait(sm, &sm.v_free[hf], (c - 1) & 1)) return false;
+            // the second half's buffer was free once the last chunk's V'^T K was done
+            if (hf == 0 && c > 0 && !wait(sm, &sm.v_free, (c - 1) & 1)) return false;
             tc_fence_after();
             const int t0 = 64 * hf + 32 * side;        // tokens t0 .. t0 + 31
-            float2 f[4];                               // factors of tokens t0 + 8 i + 2 (lane % 4)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = t0 + 8 * i + 2 * (lane & 3);
-                if (!d.slow) {
-                    const float2 x = *reinterpret_cast<const float2 *>(&d.x[t]);
-                    f[i] = fmul2(x, make_float2(d.kv, d.kv));
-                } else {
-                    f[i].x = expf((d.end_hi - d.x[t]) + (d.end_lo - d.y[t]));
-                    f[i].y = expf((d.end_hi - d.x[t + 1]) + (d.end_lo - d.y[t + 1]));
-                }
-            }
             const uint32_t vt = base + (c & 1) * kStageBytes + 2 * kTile;
             const uint32_t col = kColV + hf * kVBuf + 16 * side;
+            // 16 tokens a step, both halves of the channels.  Matrices: (tokens 0-7,
+            // channels 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+            const int ch = 32 * q + 8 * ((lane >> 3) & 1);
+            const float kv = d.kv[t0 >> 5];
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int tr = t0 + 16 * b + 8 * (lane >> 4) + (lane & 7), tt = t0 + 16 * b + 2 * (lane & 3);
+                uint32_t x[2][4];
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {              // 16 channels
-                uint32_t hi[8], mid[8], lo[8];
+                for (int a = 0; a < 2; ++a)
+                    ldmatrix_trans(vt + (ch >> 6) * kHalf + sw128_off(tr, (ch + 16 * a) & 63), x[a]);
+                float2 f[2];                           // factors of tokens tt, tt + 1 and tt + 8, tt + 9
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {          // 16 tokens
-                    // matrices: (tokens 0-7, channels 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-                    const int t = t0 + 16 * b + 8 * (lane >> 4) + (lane & 7);
-                    const int ch = 32 * q + 16 * a + 8 * ((lane >> 3) & 1);
-                    uint32_t x[4];
-                    ldmatrix_trans(vt + (ch >> 6) * kHalf + sw128_off(t, ch & 63), x);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {      // register 4 b + j: column pair 2 b + j / 2
-                        const int i = 2 * b + (j >> 1);
-                        float2 v = fmul2(bf16x2_to_float2(x[j]), f[i]);
-                        if (L < kTok) {                // 0 times whatever is there is not 0
-                            const int tt = t0 + 8 * i + 2 * (lane & 3);
-                            v.x = tt < L ? v.x : 0.f;
-                            v.y = tt + 1 < L ? v.y : 0.f;
-                        }
-                        split3(v, hi[4 * b + j], mid[4 * b + j], lo[4 * b + j]);
+                for (int i = 0; i < 2; ++i) {
+                    const int t = tt + 8 * i;
+                    const float2 dx = *reinterpret_cast<const float2 *>(&d.x[t]);
+                    if (d.mode != kDirect) {
+                        f[i] = fmul2(dx, make_float2(kv, kv));
+                    } else {
+                        f[i].x = __expf((d.end_hi - dx.x) + (d.end_lo - d.y[t]));
+                        f[i].y = __expf((d.end_hi - dx.y) + (d.end_lo - d.y[t + 1]));
                     }
                 }
-                const uint32_t at = tq + ((uint32_t)(16 * a) << 16) + col;
-                tmem_st_frag(at, hi);
-                tmem_st_frag(at + kVPart, mid);
-                tmem_st_frag(at + 2 * kVPart, lo);
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 v = fmul2(bf16x2_to_float2(x[a][j]), f[j >> 1]);
+                        split3(v, hi[j], mid[j], lo[j]);
+                    }
+                    const uint32_t at = tq + ((uint32_t)(16 * a) << 16) + col + 8 * b;
+                    tmem_st_frag(at, hi);
+                    tmem_st_frag(at + kVPart, mid);
+                    tmem_st_frag(at + 2 * kVPart, lo);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -602,42 +691,41 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 *reinterpret_cast<uint4 *>(t + sw128_off(dv, 8 * i)) = y;
             }
             fence_proxy_async_smem();
-            arrive(&sm.s_ready);
+            arrive(&sm.p_ready);
         };
         bool ok = true;
-        if (chunks > 0) {
-            ok = produce(0, 0);
-            if (ok && !kStates) publish(0);
-        }
-        for (int c = 0; ok && c < chunks; ++c) {
-            ok = produce(c, 1);
-            if (ok && c + 1 < chunks) ok = produce(c + 1, 0);
-            if (ok) ok = wait(sm, &sm.ds_full, c & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const float gamma = sm.dec[c & 1].gamma;
+#pragma unroll 1
+        for (int i = 0; ok && i <= 2 * chunks; ++i) {
+            if (i < 2 * chunks) ok = produce(i >> 1, i & 1);
+            if (!ok || (i & 1)) continue;
+            const int c = (i >> 1) - 1;                // the chunk whose V'^T K is due
+            if (c >= 0) {
+                ok = wait(sm, &sm.ds_full, c & 1);
+                if (!ok) continue;
+                tc_fence_after();
+                const float gamma = sm.dec[c & 1].gamma;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t r[32];
-                tmem_ld32(tq + kColD + dk0 + 32 * i, r);
-                tmem_wait_ld();
-                if (i == 1) {
-                    tc_fence_before();
-                    arrive(&sm.ds_free);
-                    arrive(&sm.dec_free[c & 1]);
-                }
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t r[32];
+                    tmem_ld32(tq + kColD + dk0 + 32 * b, r);
+                    tmem_wait_ld();
+                    if (b == 1) {
+                        tc_fence_before();
+                        arrive(&sm.ds_free);
+                        arrive(&sm.dec_free[c & 1]);
+                    }
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 y = ffma2(make_float2(S[32 * i + j], S[32 * i + j + 1]), make_float2(gamma, gamma),
-                                           make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
-                    S[32 * i + j] = y.x;
-                    S[32 * i + j + 1] = y.y;
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 y = ffma2(make_float2(S[32 * b + j], S[32 * b + j + 1]),
+                                               make_float2(gamma, gamma),
+                                               make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
+                        S[32 * b + j] = y.x;
+                        S[32 * b + j + 1] = y.y;
+                    }
                 }
+                if (!kStates && c + 1 < chunks) ok = wait(sm, &sm.o_full, c & 1);   // S'' has been read
             }
-            if (!kStates && c + 1 < chunks) {
-                ok = wait(sm, &sm.o_full, c & 1);      // S'' has been read
-                if (ok) publish(c + 1);
-            }
+            if (!kStates && ok && c + 1 < chunks) publish(c + 1);
         }
         float *to = nullptr;
         if (kStates) to = p.out + ((size_t)u * p.H + h) * kD * kD;

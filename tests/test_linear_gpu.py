@@ -73,6 +73,18 @@ def test_gradient(i, dtype):
     _check_bwd(x, cu, 1.0 if i % 2 else d ** -0.5)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 32), (BF, 16), (FP, 128), (FP, 32)])
+def test_sequences_of_several_segments(dtype, d):
+    """Long enough to be split on every path (256 to 1,024 tokens a segment at
+    these sizes), packed with short and empty ones, and alone."""
+    x, cu = make([1300, 0, 70, 2100], 1, 2, d, dtype, seed=d)
+    _check_fwd(x, cu)
+    _check_bwd(x, cu)
+    x, cu = make([2700], 1, 1, d, dtype, h0=False, seed=d + 1)
+    _check_fwd(x, cu)
+    _check_bwd(x, cu)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 64), (BF, 32)])
 def test_extreme_decays(dtype, d):
     """Forgetting at once (-inf), decays far below any format's range, none at
