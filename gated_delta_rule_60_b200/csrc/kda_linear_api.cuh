@@ -51,9 +51,11 @@ struct Plan {
     SegMap map;
     bool split;
     size_t state_bytes, total_bytes;                   // of one direction
+    size_t factor_bytes;                               // warp-level path: decay factors of the chunks
 };
 
-inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, int32_t d, int64_t L) {
+inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, int32_t d, int64_t L,
+                      bool factors) {
     Plan p;
     p.map.cu = cu;
     p.map.N = N;
@@ -64,6 +66,7 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
     const size_t n = (size_t)p.map.units * H;
     p.state_bytes = p.split ? align256(n * d * d * sizeof(float)) : 0;
     p.total_bytes = p.split ? align256(n * sizeof(float)) : 0;
+    p.factor_bytes = factors ? align256((size_t)(T_tot / mm::kTok + N) * H * sizeof(mm::Factors)) : 0;
     return p;
 }
 
@@ -89,7 +92,9 @@ inline int64_t fwd_length(int32_t N, bool equal, int64_t T_tot, int32_t H, int32
     return segment_length(N, equal, T_tot, (int64_t)H * (dt == KDA_FP32 && d == 128 ? 2 : 1), fwd_costs(d, dt));
 }
 
-inline size_t fwd_bytes(const Plan &p) { return p.state_bytes + p.total_bytes; }
+inline size_t fwd_bytes(const Plan &p) { return p.state_bytes + p.total_bytes + p.factor_bytes; }
+
+inline bool fwd_factors(int32_t d, kda_dtype dt) { return dt == KDA_BF16 && !tensor_path(d, dt); }
 
 inline int64_t bwd_length(int32_t N, bool equal, int64_t T_tot, int32_t H, int32_t d, kda_dtype dt) {
     return segment_length(N, equal, T_tot, H, bwd_costs(d, dt));
@@ -108,7 +113,7 @@ inline BwdSizes bwd_sizes(const Plan &p, int64_t T_tot, int32_t Hk, int32_t H, i
     s.anchors = align256(n * sizeof(double));
     s.sums = align256(n * sizeof(double));
     s.parts = Hk != H ? align256((size_t)T_tot * H * d * sizeof(float)) : 0;
-    s.all = 2 * s.states + 2 * s.totals + s.terms + s.anchors + s.sums + s.parts;
+    s.all = 2 * s.states + 2 * s.totals + s.terms + s.anchors + s.sums + s.parts + p.factor_bytes;
     return s;
 }
 
@@ -131,7 +136,7 @@ inline kda_status check_shapes(int32_t N, int64_t T_tot, int32_t Hk, int32_t H, 
     }
     if (cu == nullptr && (T_tot % N) != 0) return KDA_ERR_INVALID_ARGUMENT;
     if (cu != nullptr && !aligned16(cu)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((int64_t)N * H > 0x7fffffff || T_tot / 256 + N > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
+    if ((int64_t)N * H > 0x7fffffff || T_tot / 64 + N > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
 }
 
@@ -202,6 +207,16 @@ kda_status fwd_simt(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     return launched();
 }
 
+inline kda_status launch_factors(const Plan &p, const float *g, int per_token, int H, float scale,
+                                 mm::Factors *out, cudaStream_t s) {
+    SegMap c = p.map;
+    c.L = mm::kTok;
+    c.units = (int)(c.T_tot / mm::kTok + c.N);
+    const int64_t blocks = ((int64_t)c.units * H + 7) / 8;
+    mm::factor_kernel<<<(unsigned)blocks, 256, 0, s>>>(g, per_token, c, H, scale, out);
+    return launched();
+}
+
 // bf16 below d = 128
 template <int D>
 kda_status fwd_mma(const Plan &p, const FwdArgs &a, cudaStream_t s) {
@@ -209,21 +224,24 @@ kda_status fwd_mma(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     const unsigned blocks = (unsigned)((int64_t)p.map.units * a.H), threads = mm::Shape<D>::kThreads;
     const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q, *k = (const __nv_bfloat16 *)a.k,
                         *v = (const __nv_bfloat16 *)a.v;
+    mm::Factors *f = reinterpret_cast<mm::Factors *>(a.ws + p.state_bytes + p.total_bytes);
+    kda_status st = launch_factors(p, a.g, a.per_token, a.H, a.scale, f, s);
+    if (st != KDA_OK) return st;
     if (p.split) {
         states = reinterpret_cast<float *>(a.ws);
         total = reinterpret_cast<float *>(a.ws + p.state_bytes);
         auto kern = mm::state_kernel<D, false>;
         const size_t smem = sizeof(mm::StateSmem<D>);
         if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-        kern<<<blocks, threads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, states, total);
-        kda_status st = launched();
+        kern<<<blocks, threads, smem, s>>>(k, v, f, p.map, a.Hk, a.H, states, total);
+        st = launched();
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, total, states, s);
         if (st != KDA_OK) return st;
     }
     auto kern = mm::out_kernel<D>;
     const size_t smem = sizeof(mm::OutSmem<D>);
     if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-    kern<<<blocks, threads, smem, s>>>(q, k, v, a.g, a.per_token, a.h0, p.map, a.Hk, a.H, a.scale, states,
+    kern<<<blocks, threads, smem, s>>>(q, k, v, f, a.h0, p.map, a.Hk, a.H, a.scale, states,
                                        (__nv_bfloat16 *)a.o, a.hT);
     return launched();
 }
@@ -291,6 +309,7 @@ kda_status launch_group_sum(const float *part, void *out, int64_t T_tot, int32_t
 struct BwdSpace {
     float *S, *E, *totS, *totE, *term, *part;
     double *anchor, *sums;
+    mm::Factors *factors;
 };
 
 inline BwdSpace bwd_space(const Plan &p, const BwdSizes &z, unsigned char *w) {
@@ -307,37 +326,45 @@ inline BwdSpace bwd_space(const Plan &p, const BwdSizes &z, unsigned char *w) {
     b.term = (float *)take(z.terms);
     b.anchor = (double *)take(z.anchors);
     b.sums = (double *)take(z.sums);
-    b.part = z.parts ? (float *)w : nullptr;
+    b.part = z.parts ? (float *)take(z.parts) : nullptr;
+    b.factors = (mm::Factors *)w;
     return b;
 }
 
 // The launches of a gradient: states of both directions and their scans when the
 // sequences are split, dQ, then dK and dV; shared heads' parts are added after each.
-template <typename T, int D, typename FS, typename RS, typename KQ, typename KKV>
-kda_status launch_bwd(const Plan &p, const BwdArgs &a, FS fs, RS rs, size_t state_smem, dim3 state_grid, KQ kq,
-                      size_t q_smem, KKV kkv, size_t kv_smem, dim3 grid, unsigned threads, cudaStream_t s) {
+template <int D>
+kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
     const BwdSpace b = bwd_space(p, bwd_sizes(p, p.map.T_tot, a.Hk, a.H, D), a.ws);
-    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dO = (const T *)a.dO;
+    const float *q = (const float *)a.q, *k = (const float *)a.k, *v = (const float *)a.v, *dO = (const float *)a.dO;
     kda_status st = KDA_OK;
     if (p.split) {
-        if (!set_smem(fs, state_smem) || !set_smem(rs, state_smem)) return KDA_ERR_CUDA;
-        fs<<<state_grid, threads, state_smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, b.S, b.totS);
-        rs<<<state_grid, threads, state_smem, s>>>(q, dO, a.g, a.per_token, p.map, a.Hk, a.H, a.scale, b.E, b.totE);
+        const dim3 grid((unsigned)p.map.units, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
+        const size_t smem = sizeof(StateSmem<D>);
+        auto fs = state_kernel<float, D, false>;
+        auto rs = state_kernel<float, D, true>;
+        if (!set_smem(fs, smem) || !set_smem(rs, smem)) return KDA_ERR_CUDA;
+        fs<<<grid, kThreads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, b.S, b.totS);
+        rs<<<grid, kThreads, smem, s>>>(q, dO, a.g, a.per_token, p.map, a.Hk, a.H, a.scale, b.E, b.totE);
         st = launched();
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, b.totS, b.S, s);
         if (st == KDA_OK) st = launch_scan<true>(p, a.H, D, a.dhT, b.totE, b.E, s);
         if (st != KDA_OK) return st;
     }
-    if (!set_smem(kq, q_smem) || !set_smem(kkv, kv_smem)) return KDA_ERR_CUDA;
-    kq<<<grid, threads, q_smem, s>>>(q, k, v, dO, a.g, a.per_token, a.h0, a.dhT, p.map, a.Hk, a.H, a.scale, b.S,
-                                     b.E, (T *)a.dq, b.part, b.term, b.anchor);
+    const dim3 grid((unsigned)p.map.units, (unsigned)a.H);
+    const size_t smem = sizeof(GradSmem<D>);
+    auto kq = grad_q_kernel<float, D>;
+    auto kkv = grad_kv_kernel<float, D>;
+    if (!set_smem(kq, smem) || !set_smem(kkv, smem)) return KDA_ERR_CUDA;
+    kq<<<grid, kThreads, smem, s>>>(q, k, v, dO, a.g, a.per_token, a.h0, a.dhT, p.map, a.Hk, a.H, a.scale, b.S, b.E,
+                                    (float *)a.dq, b.part, b.term, b.anchor);
     st = launched();
-    if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dq, p.map.T_tot, a.Hk, a.H, D, s);
+    if (st == KDA_OK && b.part) st = launch_group_sum<float>(b.part, a.dq, p.map.T_tot, a.Hk, a.H, D, s);
     if (st != KDA_OK) return st;
-    kkv<<<grid, threads, kv_smem, s>>>(q, k, v, dO, a.g, a.per_token, a.dhT, p.map, a.Hk, a.H, a.scale, b.E,
-                                       b.term, b.anchor, (T *)a.dk, b.part, (T *)a.dv, a.dg, b.sums, a.dh0);
+    kkv<<<grid, kThreads, smem, s>>>(q, k, v, dO, a.g, a.per_token, a.dhT, p.map, a.Hk, a.H, a.scale, b.E, b.term,
+                                     b.anchor, (float *)a.dk, b.part, (float *)a.dv, a.dg, b.sums, a.dh0);
     st = launched();
-    if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dk, p.map.T_tot, a.Hk, a.H, D, s);
+    if (st == KDA_OK && b.part) st = launch_group_sum<float>(b.part, a.dk, p.map.T_tot, a.Hk, a.H, D, s);
     if (st == KDA_OK && !a.per_token) {
         head_sum_kernel<<<(unsigned)a.H, kThreads, 0, s>>>(b.sums, a.dg, p.map.units, a.H);
         st = launched();
@@ -346,21 +373,47 @@ kda_status launch_bwd(const Plan &p, const BwdArgs &a, FS fs, RS rs, size_t stat
 }
 
 template <int D>
-kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
-    const dim3 states((unsigned)p.map.units, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
-    return launch_bwd<float, D>(p, a, state_kernel<float, D, false>, state_kernel<float, D, true>,
-                                sizeof(StateSmem<D>), states, grad_q_kernel<float, D>, sizeof(GradSmem<D>),
-                                grad_kv_kernel<float, D>, sizeof(GradSmem<D>),
-                                dim3((unsigned)p.map.units, (unsigned)a.H), kThreads, s);
-}
-
-template <int D>
 kda_status bwd_mma(const Plan &p, const BwdArgs &a, cudaStream_t s) {
-    const dim3 grid((unsigned)((int64_t)p.map.units * a.H));
-    return launch_bwd<__nv_bfloat16, D>(p, a, mm::state_kernel<D, false>, mm::state_kernel<D, true>,
-                                        sizeof(mm::StateSmem<D>), grid, mm::grad_q_kernel<D>,
-                                        sizeof(mm::GradSmem<D>), mm::grad_kv_kernel<D>,
-                                        sizeof(mm::GradKvSmem<D>), grid, mm::Shape<D>::kThreads, s);
+    using T = __nv_bfloat16;
+    const BwdSpace b = bwd_space(p, bwd_sizes(p, p.map.T_tot, a.Hk, a.H, D), a.ws);
+    const T *q = (const T *)a.q, *k = (const T *)a.k, *v = (const T *)a.v, *dO = (const T *)a.dO;
+    const unsigned grid = (unsigned)((int64_t)p.map.units * a.H), threads = mm::Shape<D>::kThreads;
+    kda_status st = launch_factors(p, a.g, a.per_token, a.H, a.scale, b.factors, s);
+    if (st != KDA_OK) return st;
+    if (p.split) {
+        const size_t smem = sizeof(mm::StateSmem<D>);
+        auto fs = mm::state_kernel<D, false>;
+        auto rs = mm::state_kernel<D, true>;
+        if (!set_smem(fs, smem) || !set_smem(rs, smem)) return KDA_ERR_CUDA;
+        fs<<<grid, threads, smem, s>>>(k, v, b.factors, p.map, a.Hk, a.H, b.S, b.totS);
+        rs<<<grid, threads, smem, s>>>(q, dO, b.factors, p.map, a.Hk, a.H, b.E, b.totE);
+        st = launched();
+        if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, b.totS, b.S, s);
+        if (st == KDA_OK) st = launch_scan<true>(p, a.H, D, a.dhT, b.totE, b.E, s);
+        if (st != KDA_OK) return st;
+    }
+    auto kq = mm::grad_q_kernel<D>;
+    auto kkv = mm::grad_kv_kernel<D>;
+    const size_t q_smem = sizeof(mm::GradSmem<D>), kv_smem = sizeof(mm::GradKvSmem<D>);
+    if (!set_smem(kq, q_smem) || !set_smem(kkv, kv_smem)) return KDA_ERR_CUDA;
+    kq<<<grid, threads, q_smem, s>>>(q, k, v, dO, b.factors, a.h0, a.dhT, p.map, a.Hk, a.H, a.scale, b.S, b.E,
+                                     (T *)a.dq, b.part, b.term, b.anchor);
+    st = launched();
+    if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dq, p.map.T_tot, a.Hk, a.H, D, s);
+    if (st != KDA_OK) return st;
+    kkv<<<grid, threads, kv_smem, s>>>(q, k, v, dO, b.factors, a.dhT, p.map, a.Hk, a.H, a.scale, b.E, (T *)a.dk,
+                                       b.part, (T *)a.dv, b.term, a.dh0);
+    st = launched();
+    if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dk, p.map.T_tot, a.Hk, a.H, D, s);
+    if (st != KDA_OK) return st;
+    mm::decay_grad_kernel<<<dim3((unsigned)p.map.units, (unsigned)((a.H + 31) / 32)), 256, 0, s>>>(
+        b.term, b.anchor, a.per_token, p.map, a.H, a.dg, b.sums);
+    st = launched();
+    if (st == KDA_OK && !a.per_token) {
+        head_sum_kernel<<<(unsigned)a.H, kThreads, 0, s>>>(b.sums, a.dg, p.map.units, a.H);
+        st = launched();
+    }
+    return st;
 }
 
 template <typename T, int D>
@@ -408,8 +461,8 @@ extern "C" KDA_API size_t kda_linear_chunk_fwd_workspace_size(int32_t N, int64_t
     using namespace kda::lin;
     if (N <= 0 || T_tot < 0 || H <= 0 || !supported_d(d)) return 0;
     if (dt != KDA_BF16 && dt != KDA_FP32) return 0;
-    const size_t a = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, false, T_tot, H, d, dt)));
-    const size_t b = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, true, T_tot, H, d, dt)));
+    const size_t a = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, false, T_tot, H, d, dt), fwd_factors(d, dt)));
+    const size_t b = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, true, T_tot, H, d, dt), fwd_factors(d, dt)));
     return a > b ? a : b;
 }
 
@@ -428,7 +481,7 @@ extern "C" KDA_API kda_status kda_linear_chunk_fwd(
     if (T_tot == 0 && hT == nullptr) return KDA_OK;
     const kda::lin::Plan p = kda::lin::make_plan(
         cu_seqlens, N, T_tot, H, d,
-        kda::lin::fwd_length(N, cu_seqlens == nullptr, T_tot, H, d, dt));
+        kda::lin::fwd_length(N, cu_seqlens == nullptr, T_tot, H, d, dt), kda::lin::fwd_factors(d, dt));
     if ((int64_t)p.map.units * H > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
     const size_t need = kda_linear_chunk_fwd_workspace_size(N, T_tot, H, d, dt);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need ||
@@ -464,7 +517,7 @@ extern "C" KDA_API size_t kda_linear_chunk_bwd_workspace_size(int32_t N, int64_t
     if (dt != KDA_BF16 && dt != KDA_FP32) return 0;
     size_t most = 0;
     for (int equal = 0; equal < 2; ++equal) {
-        const Plan p = make_plan(nullptr, N, T_tot, H, d, bwd_length(N, equal, T_tot, H, d, dt));
+        const Plan p = make_plan(nullptr, N, T_tot, H, d, bwd_length(N, equal, T_tot, H, d, dt), dt == KDA_BF16);
         const size_t n = bwd_sizes(p, T_tot, Hk, H, d).all;
         most = n > most ? n : most;
     }
@@ -496,7 +549,7 @@ extern "C" KDA_API kda_status kda_linear_chunk_bwd(
         return KDA_ERR_INVALID_ARGUMENT;
     const kda::lin::Plan p = kda::lin::make_plan(
         cu_seqlens, N, T_tot, H, d,
-        kda::lin::bwd_length(N, cu_seqlens == nullptr, T_tot, H, d, dt));
+        kda::lin::bwd_length(N, cu_seqlens == nullptr, T_tot, H, d, dt), dt == KDA_BF16);
     if ((int64_t)p.map.units * H > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
     const size_t need = kda_linear_chunk_bwd_workspace_size(N, T_tot, Hk, H, d, dt);
     if (workspace == nullptr || workspace_bytes < need ||

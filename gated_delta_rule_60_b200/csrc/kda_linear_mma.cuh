@@ -46,10 +46,10 @@ struct __align__(16) Factors {
     float gamma;                       // e^{b_C}
     float end_hi, end_lo;
 };
+static_assert(sizeof(Factors) % 16 == 0, "copied in 16-byte pieces");
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -117,7 +117,6 @@ __device__ __forceinline__ float2 fetch_decays(const float *g, int per_token, in
                        i + 1 < L ? load_decay(g, per_token, t + i + 1, h, H) : 0.f);
 }
 
-// Factors of a chunk, by one warp.
 __device__ __forceinline__ void make_factors(Factors &f, float2 g, float scale) {
     const int lane = threadIdx.x & 31;
     Sum2 run = add2({g.x, 0.f}, {g.y, 0.f});
@@ -145,6 +144,32 @@ __device__ __forceinline__ void make_factors(Factors &f, float2 g, float scale) 
     }
 }
 
+// The factors of every chunk, one warp each, before the kernels that use them: what
+// they take is latency (a scan and a dozen exponentials), which one warp of a block
+// would make all others wait for at every chunk.  Chunk c of sequence n has the slot
+// start_n / 64 + n + c, as segments have their units.
+__global__ void __launch_bounds__(256)
+factor_kernel(const float *__restrict__ g, int per_token, SegMap chunks, int H, float scale,
+              Factors *__restrict__ out) {
+    const int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (i >= (int64_t)chunks.units * H) return;
+    const int h = (int)(i % H);
+    Segment c;
+    if (!find_segment(chunks, (int)(i / H), c)) return;
+    make_factors(out[i], fetch_decays(g, per_token, c.t0, (int)(c.t1 - c.t0), h, H), scale);
+}
+
+// The slot of a segment's first chunk.
+__device__ __forceinline__ int64_t first_slot(const SegMap &m, const Segment &s) {
+    return (s.t0 - (int64_t)s.s * m.L) / kTok + s.n + (int64_t)s.s * (m.L / kTok);
+}
+
+__device__ __forceinline__ void load_factors(Factors &f, const Factors *from) {
+    if (threadIdx.x < 32)
+        for (unsigned e = threadIdx.x; e < sizeof(Factors) / 16; e += 32)
+            cp_async16(sm100::smem_u32(&f) + 16 * e, reinterpret_cast<const char *>(from) + 16 * e, true);
+}
+
 // e^{b_i - b_j}
 __device__ __forceinline__ float spread(const Factors &f, int i, int j) {
     return expf((f.hi[i] - f.hi[j]) + (f.lo[i] - f.lo[j]));
@@ -165,14 +190,14 @@ __device__ __forceinline__ void state_times_tile(float (&acc)[8][4], const float
             else a[0][i] = sm100::pack_bf16(x.x, x.y);
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            uint32_t r[4];
-            frag_b(b, Sh::kPitch, 16 * n, 16 * k, r);
+        for (int n = 0; n < 4; n += 2) {               // four accumulators between two uses of one
+            uint32_t r[2][4];
+            frag_b(b, Sh::kPitch, 16 * n, 16 * k, r[0]);
+            frag_b(b, Sh::kPitch, 16 * n + 16, 16 * k, r[1]);
 #pragma unroll
-            for (int t = kTerms - 1; t >= 0; --t) {
-                mma(acc[2 * n], a[t], r[0], r[1]);
-                mma(acc[2 * n + 1], a[t], r[2], r[3]);
-            }
+            for (int t = kTerms - 1; t >= 0; --t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma(acc[2 * n + i], a[t], r[i >> 1][2 * (i & 1)], r[i >> 1][2 * (i & 1) + 1]);
         }
     }
 }
@@ -197,15 +222,17 @@ __device__ __forceinline__ void update_state(float (&X)[D / 8][4], uint32_t a_ti
             const float2 f = *reinterpret_cast<const float2 *>(c + 16 * k + 8 * (i >> 1) + 2 * (lane & 3));
             split3(sm100::fmul2(sm100::bf16x2_to_float2(r[i]), f), a[0][i], a[1][i], a[2][i]);
         }
+        constexpr int kB = Sh::kN >= 4 ? 2 : 1;        // pairs of n-tiles at once
 #pragma unroll
-        for (int n = 0; n < Sh::kN / 2; ++n) {
-            uint32_t b[4];
-            frag_bt(b_tile, Sh::kPitch, 16 * n, 16 * k, b);
+        for (int n = 0; n < Sh::kN / 2; n += kB) {
+            uint32_t b[kB][4];
 #pragma unroll
-            for (int t = 2; t >= 0; --t) {
-                mma(add[2 * n], a[t], b[0], b[1]);
-                mma(add[2 * n + 1], a[t], b[2], b[3]);
-            }
+            for (int i = 0; i < kB; ++i) frag_bt(b_tile, Sh::kPitch, 16 * (n + i), 16 * k, b[i]);
+#pragma unroll
+            for (int t = 2; t >= 0; --t)
+#pragma unroll
+                for (int i = 0; i < 2 * kB; ++i)
+                    mma(add[2 * n + i], a[t], b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
         }
     }
 #pragma unroll
@@ -275,9 +302,8 @@ __device__ __forceinline__ void unit_product(float (&c)[4][4], uint32_t a_tile, 
 struct Walk {
     int64_t t0, t1;
     int chunks, reverse;
-    __device__ __forceinline__ int64_t first(int i) const {
-        return t0 + (int64_t)(reverse ? chunks - 1 - i : i) * kTok;
-    }
+    __device__ __forceinline__ int chunk(int i) const { return reverse ? chunks - 1 - i : i; }
+    __device__ __forceinline__ int64_t first(int i) const { return t0 + (int64_t)chunk(i) * kTok; }
     __device__ __forceinline__ int rows(int i) const {
         const int64_t n = t1 - first(i);
         return (int)(n < kTok ? n : kTok);
@@ -322,9 +348,8 @@ struct StateSmem {
 
 template <int D, bool kReverse>
 __global__ void __launch_bounds__(Shape<D>::kThreads)
-state_kernel(const bf16 *__restrict__ x, const bf16 *__restrict__ y, const float *__restrict__ g,
-             int per_token, SegMap m, int Hk, int H, float scale, float *__restrict__ ws,
-             float *__restrict__ total) {
+state_kernel(const bf16 *__restrict__ x, const bf16 *__restrict__ y, const Factors *__restrict__ factors,
+             SegMap m, int Hk, int H, float *__restrict__ ws, float *__restrict__ total) {
     extern __shared__ __align__(16) unsigned char raw[];
     StateSmem<D> &sm = *reinterpret_cast<StateSmem<D> *>(raw);
     const int u = blockIdx.x / H, h = blockIdx.x % H;
@@ -333,31 +358,25 @@ state_kernel(const bf16 *__restrict__ x, const bf16 *__restrict__ y, const float
     if (sg.s == (kReverse ? 0 : sg.count - 1)) return;
     const Walk w = make_walk(sg, kReverse);
     const int hk = h / (H / Hk);
+    const int64_t slot = first_slot(m, sg);
     float X[D / 8][4];
     load_state<D, false>(X, nullptr);
     Sum2 sum = {0.f, 0.f};
     auto load = [&](int i) {
         load_tile<D>(sm100::smem_u32(sm.a[i & 1]), x, w.first(i), w.rows(i), Hk, hk);
         load_tile<D>(sm100::smem_u32(sm.b[i & 1]), y, w.first(i), w.rows(i), H, h);
+        load_factors(sm.f[i & 1], factors + (slot + w.chunk(i)) * H + h);
         cp_commit();
     };
     load(0);
-    if (threadIdx.x < 32)
-        make_factors(sm.f[0], fetch_decays(g, per_token, w.first(0), w.rows(0), h, H), scale);
     for (int i = 0; i < w.chunks; ++i) {
         cp_wait_all();
         __syncthreads();
-        const bool more = i + 1 < w.chunks;
-        float2 next = make_float2(0.f, 0.f);
-        if (more) {
-            load(i + 1);
-            if (threadIdx.x < 32) next = fetch_decays(g, per_token, w.first(i + 1), w.rows(i + 1), h, H);
-        }
+        if (i + 1 < w.chunks) load(i + 1);
         const Factors &f = sm.f[i & 1];
         update_state<D>(X, sm100::smem_u32(sm.a[i & 1]), sm100::smem_u32(sm.b[i & 1]), kReverse ? f.row : f.col,
                         f.gamma);
         sum = add2(sum, {f.end_hi, f.end_lo});
-        if (more && threadIdx.x < 32) make_factors(sm.f[(i + 1) & 1], next, scale);
     }
     store_state<D, false>(X, ws + ((size_t)u * H + h) * D * D);
     if (threadIdx.x == 0) total[(size_t)u * H + h] = exp_sum(sum);
@@ -375,7 +394,7 @@ struct OutSmem {
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads)
 out_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
-           const float *__restrict__ g, int per_token, const float *h0, SegMap m, int Hk, int H,
+           const Factors *__restrict__ factors, const float *h0, SegMap m, int Hk, int H,
            float scale, const float *__restrict__ ws, bf16 *__restrict__ o, float *hT) {
     using Sh = Shape<D>;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -386,6 +405,7 @@ out_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *_
     if (!find_segment(m, u, sg)) return;
     const Walk w = make_walk(sg, false);
     const int hk = h / (H / Hk), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int64_t slot = first_slot(m, sg);
     const float *from = ws != nullptr && sg.count > 1 ? ws + ((size_t)u * H + h) * D * D
                         : h0 != nullptr ? h0 + ((size_t)sg.n * H + h) * D * D : nullptr;
     float X[D / 8][4];
@@ -396,23 +416,15 @@ out_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *_
         load_tile<D>(sm100::smem_u32(sm.q[i & 1]), q, t, L, Hk, hk);
         load_tile<D>(sm100::smem_u32(sm.k[i & 1]), k, t, L, Hk, hk);
         load_tile<D>(sm100::smem_u32(sm.v[i & 1]), v, t, L, H, h);
+        load_factors(sm.f[i & 1], factors + (slot + w.chunk(i)) * H + h);
         cp_commit();
     };
-    if (w.chunks > 0) {
-        load(0);
-        if (threadIdx.x < 32)
-            make_factors(sm.f[0], fetch_decays(g, per_token, w.first(0), w.rows(0), h, H), scale);
-    }
+    if (w.chunks > 0) load(0);
     const uint32_t tp = sm100::smem_u32(sm.p);
     for (int i = 0; i < w.chunks; ++i) {
         cp_wait_all();
         __syncthreads();
-        const bool more = i + 1 < w.chunks;
-        float2 next = make_float2(0.f, 0.f);
-        if (more) {
-            load(i + 1);
-            if (threadIdx.x < 32) next = fetch_decays(g, per_token, w.first(i + 1), w.rows(i + 1), h, H);
-        }
+        if (i + 1 < w.chunks) load(i + 1);
         const Factors &f = sm.f[i & 1];
         const uint32_t tq = sm100::smem_u32(sm.q[i & 1]), tk = sm100::smem_u32(sm.k[i & 1]),
                        tv = sm100::smem_u32(sm.v[i & 1]);
@@ -460,7 +472,6 @@ out_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *_
             for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(in[n][e], scale, acc[n][e]);
         store_transposed<D>(acc, o, nullptr, w.first(i), w.rows(i), H, h, 1.f);
         update_state<D>(X, tv, tk, f.col, f.gamma);
-        if (more && threadIdx.x < 32) make_factors(sm.f[(i + 1) & 1], next, scale);
     }
     if (hT != nullptr && sg.s == sg.count - 1)
         store_state<D, true>(X, hT + ((size_t)sg.n * H + h) * D * D);
@@ -577,7 +588,7 @@ __device__ __forceinline__ void scale_and_dot(float (&acc)[8][4], const float *f
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads)
 grad_q_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
-              const bf16 *__restrict__ dO, const float *__restrict__ g, int per_token,
+              const bf16 *__restrict__ dO, const Factors *__restrict__ factors,
               const float *__restrict__ h0, const float *__restrict__ dhT, SegMap m, int Hk, int H,
               float scale, const float *__restrict__ wsS, const float *__restrict__ wsE,
               bf16 *__restrict__ dq, float *__restrict__ part, float *__restrict__ term,
@@ -591,6 +602,7 @@ grad_q_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16
     if (!find_segment(m, u, sg)) return;
     const Walk w = make_walk(sg, false);
     const int hk = h / (H / Hk), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int64_t slot = first_slot(m, sg);
     const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
     float X[D / 8][4];
     load_state<D, false>(X, wsS != nullptr && sg.count > 1 ? wsS + seg : h0 != nullptr ? h0 + seq : nullptr);
@@ -601,22 +613,15 @@ grad_q_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16
         load_tile<D>(sm100::smem_u32(sm.k[i & 1]), k, t, L, Hk, hk);
         load_tile<D>(sm100::smem_u32(sm.v[i & 1]), v, t, L, H, h);
         load_tile<D>(sm100::smem_u32(sm.dO[i & 1]), dO, t, L, H, h);
+        load_factors(sm.f[i & 1], factors + (slot + w.chunk(i)) * H + h);
         cp_commit();
     };
-    if (w.chunks > 0) {
-        load(0);
-        if (warp == 0) make_factors(sm.f[0], fetch_decays(g, per_token, w.first(0), w.rows(0), h, H), scale);
-    }
+    if (w.chunks > 0) load(0);
     const uint32_t ta = sm100::smem_u32(sm.a);
     for (int i = 0; i < w.chunks; ++i) {
         cp_wait_all();
         __syncthreads();
-        const bool more = i + 1 < w.chunks;
-        float2 next = make_float2(0.f, 0.f);
-        if (more) {
-            load(i + 1);
-            if (warp == 0) next = fetch_decays(g, per_token, w.first(i + 1), w.rows(i + 1), h, H);
-        }
+        if (i + 1 < w.chunks) load(i + 1);
         const Factors &f = sm.f[i & 1];
         const uint32_t tq = sm100::smem_u32(sm.q[i & 1]), tk = sm100::smem_u32(sm.k[i & 1]),
                        tv = sm100::smem_u32(sm.v[i & 1]), td = sm100::smem_u32(sm.dO[i & 1]);
@@ -647,7 +652,6 @@ grad_q_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16
             term[(size_t)(t + r) * H + h] = s;
         }
         update_state<D>(X, tk, tv, f.col, f.gamma);
-        if (more && warp == 0) make_factors(sm.f[(i + 1) & 1], next, scale);
     }
     const float *to = wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
     double s = 0.0;
@@ -670,27 +674,23 @@ grad_q_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16
     }
 }
 
-// dK, dV, dg and dh0, chunks last to first.
+// dK, dV, y_j = k_j . dk_j and dh0, chunks last to first.
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads)
 grad_kv_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *__restrict__ v,
-               const bf16 *__restrict__ dO, const float *__restrict__ g, int per_token,
+               const bf16 *__restrict__ dO, const Factors *__restrict__ factors,
                const float *__restrict__ dhT, SegMap m, int Hk, int H, float scale,
-               const float *__restrict__ wsE, const float *__restrict__ term,
-               const double *__restrict__ anchor, bf16 *__restrict__ dk, float *__restrict__ part,
-               bf16 *__restrict__ dv, float *__restrict__ dg, double *__restrict__ head_sum,
-               float *__restrict__ dh0) {
+               const float *__restrict__ wsE, bf16 *__restrict__ dk, float *__restrict__ part,
+               bf16 *__restrict__ dv, float *__restrict__ term, float *__restrict__ dh0) {
     using Sh = Shape<D>;
     extern __shared__ __align__(16) unsigned char raw[];
     GradKvSmem<D> &sm = *reinterpret_cast<GradKvSmem<D> *>(raw);
     const int u = blockIdx.x / H, h = blockIdx.x % H;
     Segment sg;
-    if (!find_segment(m, u, sg)) {
-        if (!per_token && threadIdx.x == 0) head_sum[(size_t)u * H + h] = 0.0;
-        return;
-    }
+    if (!find_segment(m, u, sg)) return;
     const Walk w = make_walk(sg, true);
     const int hk = h / (H / Hk), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int64_t slot = first_slot(m, sg);
     const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
     float X[D / 8][4];
     load_state<D, false>(X, wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr);
@@ -701,25 +701,17 @@ grad_kv_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf1
         load_tile<D>(sm100::smem_u32(sm.k[i & 1]), k, t, L, Hk, hk);
         load_tile<D>(sm100::smem_u32(sm.v[i & 1]), v, t, L, H, h);
         load_tile<D>(sm100::smem_u32(sm.dO[i & 1]), dO, t, L, H, h);
+        load_factors(sm.f[i & 1], factors + (slot + w.chunk(i)) * H + h);
         cp_commit();
     };
-    if (w.chunks > 0) {
-        load(0);
-        if (warp == 0) make_factors(sm.f[0], fetch_decays(g, per_token, w.first(0), w.rows(0), h, H), scale);
-    }
+    if (w.chunks > 0) load(0);
     const uint32_t ta = sm100::smem_u32(sm.a), tp = sm100::smem_u32(sm.p), te = sm100::smem_u32(sm.e);
-    double carry = anchor[(size_t)u * H + h], sum = 0.0;   // warp 0
     for (int i = 0; i < w.chunks; ++i) {
         const int64_t t = w.first(i);
         const int L = w.rows(i);
         cp_wait_all();
         __syncthreads();
-        const bool more = i + 1 < w.chunks;
-        float2 next = make_float2(0.f, 0.f);
-        if (more) {
-            load(i + 1);
-            if (warp == 0) next = fetch_decays(g, per_token, w.first(i + 1), w.rows(i + 1), h, H);
-        }
+        if (i + 1 < w.chunks) load(i + 1);
         const Factors &f = sm.f[i & 1];
         const uint32_t tq = sm100::smem_u32(sm.q[i & 1]), tk = sm100::smem_u32(sm.k[i & 1]),
                        tv = sm100::smem_u32(sm.v[i & 1]), td = sm100::smem_u32(sm.dO[i & 1]);
@@ -797,41 +789,64 @@ grad_kv_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf1
                             sm100::pack_bf16(c[n][2 * hf], c[n][2 * hf + 1]);
                 }
         }
-        if (warp == 0) {                               // sums from the chunk's end
-            double y[2];
-            int r[2];
+        for (int r = threadIdx.x; r < L; r += Sh::kThreads) {
+            float y = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {              // lane 0 holds the last two tokens
-                r[e] = kTok - 1 - 2 * lane - e;
-                double s = 0.0;
-                if (r[e] < L) {
-                    float b = 0.f;
+            for (int z = 0; z < 4; ++z) y += sm.inner[z][r];
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) b += sm.inner[z][r[e]];
-#pragma unroll
-                    for (int z = 0; z < Sh::kWarps; ++z) b += sm.outer[z][r[e]];
-                    s = (double)term[(size_t)(t + r[e]) * H + h] - (double)b;
-                }
-                y[e] = s;
-            }
-            const double both = warp_scan(y[0] + y[1]), before = both - (y[0] + y[1]) + carry;
-            const double d0 = before + y[0], d1 = d0 + y[1];
-            if (per_token) {
-                if (r[0] < L) dg[(size_t)(t + r[0]) * H + h] = (float)d0;
-                if (r[1] < L) dg[(size_t)(t + r[1]) * H + h] = (float)d1;
-            }
-            sum += (r[0] < L ? d0 : 0.0) + (r[1] < L ? d1 : 0.0);
-            carry = __shfl_sync(0xffffffffu, d1, 31);
+            for (int z = 0; z < Sh::kWarps; ++z) y += sm.outer[z][r];
+            term[(size_t)(t + r) * H + h] -= y;        // x of the other walk, minus y
         }
         update_state<D>(X, tq, td, f.row, f.gamma);
-        if (more && warp == 0) make_factors(sm.f[(i + 1) & 1], next, scale);
-    }
-    if (!per_token && warp == 0) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) head_sum[(size_t)u * H + h] = sum;
     }
     if (dh0 != nullptr && sg.s == 0) store_state<D, false>(X, dh0 + seq);
+}
+
+// dg_t = sum over the segment's tokens from t on of (x - y), plus <S_end, E_end>:
+// lanes are heads, the 8 warps of a block take an eighth of the tokens each (their
+// totals first), sums in fp64.  With a constant decay the segment's sum goes out.
+__global__ void __launch_bounds__(256)
+decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anchor, int per_token, SegMap m,
+                  int H, float *__restrict__ dg, double *__restrict__ head_sum) {
+    __shared__ double total[8][33];
+    const int u = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int h = blockIdx.y * 32 + lane;
+    Segment sg;
+    const bool live = find_segment(m, u, sg);
+    if (!live) {
+        if (!per_token && warp == 0 && h < H) head_sum[(size_t)u * H + h] = 0.0;
+        return;
+    }
+    const int64_t len = sg.t1 - sg.t0, per = (len + 7) / 8;
+    const int64_t a = sg.t0 + warp * per < sg.t1 ? sg.t0 + warp * per : sg.t1;
+    const int64_t b = a + per < sg.t1 ? a + per : sg.t1;
+    double s = 0.0;
+    if (h < H) {
+#pragma unroll 8
+        for (int64_t t = b - 1; t >= a; --t) s += (double)term[(size_t)t * H + h];
+    }
+    total[warp][lane] = s;
+    __syncthreads();
+    s = h < H ? anchor[(size_t)u * H + h] : 0.0;
+    for (int i = 7; i > warp; --i) s += total[i][lane];
+    double all = 0.0;
+    if (h < H) {
+#pragma unroll 8
+        for (int64_t t = b - 1; t >= a; --t) {
+            s += (double)term[(size_t)t * H + h];
+            if (per_token) dg[(size_t)t * H + h] = (float)s;
+            all += s;
+        }
+    }
+    if (per_token) return;
+    __syncthreads();
+    total[warp][lane] = all;
+    __syncthreads();
+    if (warp == 0 && h < H) {
+        all = 0.0;
+        for (int i = 0; i < 8; ++i) all += total[i][lane];
+        head_sum[(size_t)u * H + h] = all;
+    }
 }
 
 }  // namespace mm
