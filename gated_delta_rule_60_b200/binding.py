@@ -11,8 +11,8 @@ The Python names are the C names.  As in the C ABI, the tensors of a call
 must live on the current CUDA device (select it with torch.cuda.set_device or
 a torch.cuda.device context); stream=None means that device's current stream.
 """
-import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -514,56 +514,96 @@ def kda_debug_range_read() -> dict:
             for i, r in enumerate(RANGE_ROWS)}
 
 
-def _current(t: torch.Tensor, name: str):
-    """The device of t, which has to be the current CUDA device (the launch
-    goes there whatever the tensors say)."""
+# The calls below serve single tokens too, where a call's own time counts: they
+# hand plain integers to ctypes and ask torch for the raw stream and device.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _index(t: torch.Tensor, name: str) -> int:
+    """The device index of t, which has to be the current CUDA device (the
+    launch goes there whatever the tensors say)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError("%s must be on cuda, got %s" % (name, dev))
-    if dev.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, which is not the current device" % (name, dev))
-    return dev
+    idx = t.get_device()
+    if idx < 0:
+        raise ValueError("%s must be on cuda, got %s" % (name, t.device))
+    if idx != _current_device():
+        raise ValueError("%s is on %s, which is not the current device" % (name, t.device))
+    return idx
 
 
-def _on(stream):
-    """Where a call allocates: torch's memory belongs to a stream, so what a
-    call on another stream writes has to come from that stream's."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _at(t, name: str, dtype, shape, idx: int) -> int:
+    """The address of a dense tensor of this type, shape and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.get_device() == idx and t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, shape, torch.device("cuda", idx))
+    return t.data_ptr()
 
 
-def _workspace(need: int, given: Optional[torch.Tensor], dev):
-    """(pointer, bytes, tensor) of a call's scratch: the caller's, or a new one."""
+def _maybe(t, name: str, dtype, shape, idx: int):
+    return None if t is None else _at(t, name, dtype, shape, idx)
+
+
+def _stream_at(stream, idx: int) -> int:
+    if stream is None:
+        return _raw_stream(idx)
+    if stream.device.index != idx:
+        raise ValueError("stream is on %s, the tensors on cuda:%d" % (stream.device, idx))
+    return stream.cuda_stream
+
+
+def _empty(stream, idx: int, shape, dtype) -> torch.Tensor:
+    """Memory for a call on `stream`: torch's memory belongs to a stream, so what a
+    call on another one writes has to come from that stream's."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=idx)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=idx)
+
+
+def _workspace(need: int, given: Optional[torch.Tensor], stream, idx: int):
+    """(address, bytes, tensor) of a call's scratch: the caller's, or a new one."""
     if given is None:
         if not need:
             return None, 0, None
-        given = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif given.device != dev or not given.is_contiguous():
-        raise ValueError("workspace must be contiguous on %s" % dev)
-    return _ptr(given), given.numel() * given.element_size(), given
+        given = _empty(stream, idx, need, torch.uint8)
+        return given.data_ptr(), need, given
+    if given.get_device() != idx or not given.is_contiguous():
+        raise ValueError("workspace must be contiguous on cuda:%d" % idx)
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
-def _linear_sizes(q, v, g, cu_seqlens, num_seqs):
-    """(device, T, Hk, H, d, dtype, N, g_per_token) of a linear-attention call."""
-    dev = _current(q, "q")
+def _seqs(cu_seqlens, num_seqs, idx: int):
+    """(address of cu_seqlens or None, number of sequences)"""
+    if cu_seqlens is None:
+        return None, 1 if num_seqs is None else int(num_seqs)
+    n = cu_seqlens.numel() if isinstance(cu_seqlens, torch.Tensor) else 0
+    return _at(cu_seqlens, "cu_seqlens", torch.int32, (n,), idx), n - 1
+
+
+def _linear_sizes(q, v, g):
+    """(device, T, Hk, H, d, dtype, its code, address of g, g_per_token)"""
+    idx = _index(q, "q")
     if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("q, k and v must have three dimensions")
     T, Hk, d = q.shape
     H = v.shape[1]
-    dt = q.dtype
-    if dt not in _DTYPES:
-        raise TypeError("unsupported dtype %s" % dt)
-    if cu_seqlens is not None:
-        _check(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
-        N = cu_seqlens.numel() - 1
-    else:
-        N = 1 if num_seqs is None else int(num_seqs)
+    code = _DTYPES.get(q.dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % q.dtype)
     if not isinstance(g, torch.Tensor):
         raise TypeError("g must be a torch.Tensor")
     per_token = g.dim() == 2
-    _check(g, "g", torch.float32, (T, H) if per_token else (H,), dev)
-    return dev, T, Hk, H, d, dt, N, int(per_token)
+    return idx, T, Hk, H, d, q.dtype, code, _at(g, "g", torch.float32, (T, H) if per_token else (H,), idx), \
+        int(per_token)
+
+
+@functools.lru_cache(maxsize=1024)
+def _size(name: str, *sizes) -> int:
+    """A workspace query: a pure function of the sizes."""
+    return int(getattr(load_library(), name)(*sizes))
 
 
 def kda_linear_chunk_fwd_workspace_size(N: int, T_tot: int, H: int, d: int,
@@ -596,26 +636,22 @@ def kda_linear_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     with num_seqs sequences of equal length.
     """
     lib = load_library()
-    dev, T, Hk, H, d, dt, N, per_token = _linear_sizes(q, v, g, cu_seqlens, num_seqs)
-    _check(q, "q", dt, (T, Hk, d), dev)
-    _check(k, "k", dt, (T, Hk, d), dev)
-    _check(v, "v", dt, (T, H, d), dev)
-    if h0 is not None:
-        _check(h0, "h0", torch.float32, (N, H, d, d), dev)
-    if o is not None:
-        _check(o, "o", dt, (T, H, d), dev)
-    if hT is not None:
-        _check(hT, "hT", torch.float32, (N, H, d, d), dev)
-    need = lib.kda_linear_chunk_fwd_workspace_size(N, T, H, d, _DTYPES[dt])
-    with _on(stream):
-        if o is None:
-            o = torch.empty(T, H, d, dtype=dt, device=dev)
-        if hT is None and output_final_state:
-            hT = torch.empty(N, H, d, d, dtype=torch.float32, device=dev)
-        ws, ws_bytes, _keep = _workspace(need, workspace, dev)
-    st = lib.kda_linear_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(cu_seqlens),
-                                  N, T, Hk, H, d, _DTYPES[dt], per_token, float(scale), _ptr(o),
-                                  _ptr(hT), ws, ws_bytes, _stream_handle(stream))
+    idx, T, Hk, H, d, dt, code, pg, per_token = _linear_sizes(q, v, g)
+    cu, N = _seqs(cu_seqlens, num_seqs, idx)
+    pq, pk = _at(q, "q", dt, (T, Hk, d), idx), _at(k, "k", dt, (T, Hk, d), idx)
+    pv = _at(v, "v", dt, (T, H, d), idx)
+    state = (N, H, d, d)
+    ph = _maybe(h0, "h0", torch.float32, state, idx)
+    handle = _stream_at(stream, idx)
+    if o is None:
+        o = _empty(stream, idx, (T, H, d), dt)
+    if hT is None and output_final_state and N >= 0:
+        hT = _empty(stream, idx, state, torch.float32)
+    ws, ws_bytes, _keep = _workspace(_size("kda_linear_chunk_fwd_workspace_size", N, T, H, d, code),
+                                     workspace, stream, idx)
+    st = lib.kda_linear_chunk_fwd(pq, pk, pv, pg, ph, cu, N, T, Hk, H, d, code, per_token, scale,
+                                  _at(o, "o", dt, (T, H, d), idx),
+                                  _maybe(hT, "hT", torch.float32, state, idx), ws, ws_bytes, handle)
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_chunk_fwd")
     return o, hT
@@ -628,19 +664,14 @@ def kda_linear_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     fp32 is updated in place.  q, k [B, Hk, d], v [B, H, d], g fp32 [B, H] or
     [H].  Returns o [B, H, d]."""
     lib = load_library()
-    dev, B, Hk, H, d, dt, _, per_token = _linear_sizes(q, v, g, None, 1)
-    _check(q, "q", dt, (B, Hk, d), dev)
-    _check(k, "k", dt, (B, Hk, d), dev)
-    _check(v, "v", dt, (B, H, d), dev)
-    _check(S, "S", torch.float32, (B, H, d, d), dev)
-    if o is not None:
-        _check(o, "o", dt, (B, H, d), dev)
-    else:
-        with _on(stream):
-            o = torch.empty(B, H, d, dtype=dt, device=dev)
-    st = lib.kda_linear_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(o), B, Hk, H,
-                                    d, _DTYPES[dt], per_token, float(scale),
-                                    _stream_handle(stream))
+    idx, B, Hk, H, d, dt, code, pg, per_token = _linear_sizes(q, v, g)
+    pq, pk = _at(q, "q", dt, (B, Hk, d), idx), _at(k, "k", dt, (B, Hk, d), idx)
+    pv, pS = _at(v, "v", dt, (B, H, d), idx), _at(S, "S", torch.float32, (B, H, d, d), idx)
+    handle = _stream_at(stream, idx)
+    if o is None:
+        o = _empty(stream, idx, (B, H, d), dt)
+    st = lib.kda_linear_decode_step(pq, pk, pv, pg, pS, _at(o, "o", dt, (B, H, d), idx), B, Hk, H, d,
+                                    code, per_token, scale, handle)
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_decode_step")
     return o
@@ -656,27 +687,22 @@ def kda_linear_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: t
     dq, dk [T, Hk, d], dv [T, H, d] (dtype of q), dg fp32 of g's shape and
     dh0 [N, H, d, d] fp32."""
     lib = load_library()
-    dev, T, Hk, H, d, dt, N, per_token = _linear_sizes(q, v, g, cu_seqlens, num_seqs)
-    _check(q, "q", dt, (T, Hk, d), dev)
-    _check(k, "k", dt, (T, Hk, d), dev)
-    _check(v, "v", dt, (T, H, d), dev)
-    _check(dO, "dO", dt, (T, H, d), dev)
-    for t, name in ((h0, "h0"), (dhT, "dhT")):
-        if t is not None:
-            _check(t, name, torch.float32, (N, H, d, d), dev)
-    need = lib.kda_linear_chunk_bwd_workspace_size(N, T, Hk, H, d, _DTYPES[dt])
-    with _on(stream):
-        out = {"dq": torch.empty(T, Hk, d, dtype=dt, device=dev),
-               "dk": torch.empty(T, Hk, d, dtype=dt, device=dev),
-               "dv": torch.empty(T, H, d, dtype=dt, device=dev),
-               "dg": torch.empty(g.shape, dtype=torch.float32, device=dev),
-               "dh0": torch.empty(N, H, d, d, dtype=torch.float32, device=dev)}
-        ws, ws_bytes, _keep = _workspace(need, workspace, dev)
-    st = lib.kda_linear_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(h0), _ptr(cu_seqlens),
-                                  N, T, Hk, H, d, _DTYPES[dt], per_token, float(scale), _ptr(dO),
-                                  _ptr(dhT), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-                                  _ptr(out["dg"]), _ptr(out["dh0"]), ws, ws_bytes,
-                                  _stream_handle(stream))
+    idx, T, Hk, H, d, dt, code, pg, per_token = _linear_sizes(q, v, g)
+    cu, N = _seqs(cu_seqlens, num_seqs, idx)
+    pq, pk = _at(q, "q", dt, (T, Hk, d), idx), _at(k, "k", dt, (T, Hk, d), idx)
+    pv, pd = _at(v, "v", dt, (T, H, d), idx), _at(dO, "dO", dt, (T, H, d), idx)
+    state = (max(N, 0), H, d, d)
+    ph, pT = _maybe(h0, "h0", torch.float32, state, idx), _maybe(dhT, "dhT", torch.float32, state, idx)
+    handle = _stream_at(stream, idx)
+    out = {"dq": _empty(stream, idx, (T, Hk, d), dt), "dk": _empty(stream, idx, (T, Hk, d), dt),
+           "dv": _empty(stream, idx, (T, H, d), dt),
+           "dg": _empty(stream, idx, g.shape, torch.float32),
+           "dh0": _empty(stream, idx, state, torch.float32)}
+    ws, ws_bytes, _keep = _workspace(
+        _size("kda_linear_chunk_bwd_workspace_size", N, T, Hk, H, d, code), workspace, stream, idx)
+    p = {n: t.data_ptr() for n, t in out.items()}
+    st = lib.kda_linear_chunk_bwd(pq, pk, pv, pg, ph, cu, N, T, Hk, H, d, code, per_token, scale, pd, pT,
+                                  p["dq"], p["dk"], p["dv"], p["dg"], p["dh0"], ws, ws_bytes, handle)
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_chunk_bwd")
     return out
@@ -707,22 +733,26 @@ def kda_rotary_frequencies(rot: int, base: float = 10000.0, scaling: int = KDA_R
     return inv.to("cuda" if device is None else device), float(scale.value)
 
 
-def _token_rows(t: torch.Tensor, name: str, dt, T: int, d: int, dev) -> int:
-    """Elements between the tokens of a [T, heads, d] tensor whose token rows
-    are dense (the tokens themselves may be apart: a slice of a projection)."""
+def _token_rows(t: torch.Tensor, name: str, dt, T: int, d: int, idx: int):
+    """(address, heads, elements between tokens) of a [T, heads, d] tensor
+    whose token rows are dense (the tokens themselves may be apart: a slice of
+    a projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device != dev:
-        raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
-    if t.dtype != dt:
+    if t.get_device() != idx:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, idx, t.device))
+    if t.dtype is not dt:
         raise TypeError("%s must be %s, got %s" % (name, dt, t.dtype))
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
-        raise ValueError("%s must have shape (%d, heads, %d), got %s" % (name, T, d,
-                                                                         tuple(t.shape)))
-    s, heads = t.stride(), t.shape[1]
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d:
+        raise ValueError("%s must have shape (%d, heads, %d), got %s" % (name, T, d, tuple(shape)))
+    heads = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), heads, heads * d
+    s = t.stride()
     if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d) or (T > 1 and s[0] < heads * d):
         raise ValueError("%s must have dense heads, got strides %s" % (name, s))
-    return s[0] if T > 1 else heads * d
+    return t.data_ptr(), heads, s[0] if T > 1 else heads * d
 
 
 def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
@@ -740,71 +770,65 @@ def kda_rotary(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: Optional[to
     cu_seqlens / num_seqs.  inverse turns back, which is also the gradient.
     """
     lib = load_library()
-    dev = _current(q, "q")
+    idx = _index(q, "q")
     if q.dim() != 3:
         raise ValueError("q must have three dimensions")
     T, Hq, d = q.shape
     dt = q.dtype
-    if dt not in _DTYPES:
+    code = _DTYPES.get(dt)
+    if code is None:
         raise TypeError("unsupported dtype %s" % dt)
-    sq = _token_rows(q, "q", dt, T, d, dev)
-    rot = 0
+    pq, _, sq = _token_rows(q, "q", dt, T, d, idx)
+    rot, pf = 0, None
     if inv_freq is not None:
-        _check(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev)
         rot = 2 * inv_freq.numel()
-    if positions is not None:
-        _check(positions, "positions", torch.int32, (T,), dev)
-    if cu_seqlens is not None:
-        _check(cu_seqlens, "cu_seqlens", torch.int32, (cu_seqlens.numel(),), dev)
-        N = cu_seqlens.numel() - 1
-    else:
-        N = 1 if num_seqs is None else int(num_seqs)
+        pf = _at(inv_freq, "inv_freq", torch.float32, (rot // 2,), idx)
+    pp = _maybe(positions, "positions", torch.int32, (T,), idx)
+    cu, N = _seqs(cu_seqlens, num_seqs, idx)
+    handle = _stream_at(stream, idx)
     if q_out is None:
-        with _on(stream):
-            q_out = torch.empty(T, Hq, d, dtype=dt, device=dev)
-    elif tuple(q_out.shape) != (T, Hq, d):
+        q_out = _empty(stream, idx, (T, Hq, d), dt)
+    pqo, heads, sqo = _token_rows(q_out, "q_out", dt, T, d, idx)
+    if heads != Hq:
         raise ValueError("q_out must have shape %s" % ((T, Hq, d),))
+    pk = pko = None
     Hk = sk = sko = 0
     if k is not None:
-        sk = _token_rows(k, "k", dt, T, d, dev)
-        Hk = k.shape[1]
+        pk, Hk, sk = _token_rows(k, "k", dt, T, d, idx)
         if k_out is None:
-            with _on(stream):
-                k_out = torch.empty(T, Hk, d, dtype=dt, device=dev)
-        elif tuple(k_out.shape) != (T, Hk, d):
+            k_out = _empty(stream, idx, (T, Hk, d), dt)
+        pko, heads, sko = _token_rows(k_out, "k_out", dt, T, d, idx)
+        if heads != Hk:
             raise ValueError("k_out must have shape %s" % ((T, Hk, d),))
-        sko = _token_rows(k_out, "k_out", dt, T, d, dev)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    st = lib.kda_rotary(_ptr(q), _ptr(k), _ptr(inv_freq), _ptr(positions), _ptr(cu_seqlens), N, T,
-                        Hq, Hk, d, rot, _DTYPES[dt], int(bool(interleaved)), int(bool(inverse)),
-                        float(scale), sq, sk, _ptr(q_out), _ptr(k_out),
-                        _token_rows(q_out, "q_out", dt, T, d, dev), sko, _stream_handle(stream))
+    st = lib.kda_rotary(pq, pk, pf, pp, cu, N, T, Hq, Hk, d, rot, code, int(bool(interleaved)),
+                        int(bool(inverse)), scale, sq, sk, pqo, pko, sqo, sko, handle)
     if st != KDA_OK:
         raise KdaError(st, "kda_rotary")
     return q_out, k_out
 
 
 def _norm_sizes(x, weight):
-    """(device, T, G, D, dtype): weight [D] norms the last axis, [G, D] the
-    last axis of x [..., G, D] with a row for each of G."""
-    dev = _current(x, "x")
-    if x.dim() < 1:
+    """(device, T, G, D, dtype, its code): weight [D] norms the last axis,
+    [G, D] the last axis of x [..., G, D] with a row for each of G."""
+    idx = _index(x, "x")
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must have a last axis")
-    dt = x.dtype
-    if dt not in _DTYPES:
-        raise TypeError("unsupported dtype %s" % dt)
-    D = x.shape[-1]
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % x.dtype)
+    D = shape[-1]
     G = 1
     if weight is not None and weight.dim() == 2:
         G = weight.shape[0]
-        if x.dim() < 2 or x.shape[-2] != G:
+        if len(shape) < 2 or shape[-2] != G:
             raise ValueError("a weight of shape %s needs x of shape (..., %d, %d)" % (
                 tuple(weight.shape), G, D))
     if D == 0 or G == 0:
         raise ValueError("x must have a last axis")
-    _check(x, "x", dt, x.shape, dev)
-    return dev, x.numel() // (G * D), G, D, dt
+    return idx, x.numel() // (G * D), G, D, x.dtype, code
 
 
 def kda_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -815,21 +839,19 @@ def kda_layernorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     of x's shape without that axis.  weight, bias fp32 [D], or [G, D] with a
     row for each of the G in x [..., G, D] (heads); y may be x."""
     lib = load_library()
-    dev, T, G, D, dt = _norm_sizes(x, weight if weight is not None else bias)
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _check(t, name, torch.float32, (G, D) if t.dim() == 2 else (D,), dev)
-            if t.numel() != G * D:
-                raise ValueError("weight and bias must have one shape")
-    if y is not None:
-        _check(y, "y", dt, x.shape, dev)
-    with _on(stream):
-        if y is None:
-            y = torch.empty_like(x)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    st = lib.kda_layernorm_fwd(_ptr(x), _ptr(weight), _ptr(bias), T, G, D, _DTYPES[dt], float(eps),
-                               _ptr(y), _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    by = weight if weight is not None else bias
+    idx, T, G, D, dt, code = _norm_sizes(x, by)
+    shape = x.shape
+    px = _at(x, "x", dt, shape, idx)
+    of = None if by is None else (D,) if by.dim() != 2 else (G, D)
+    pw, pb = _maybe(weight, "weight", torch.float32, of, idx), _maybe(bias, "bias", torch.float32, of, idx)
+    handle = _stream_at(stream, idx)
+    if y is None:
+        y = _empty(stream, idx, shape, dt)
+    mean = _empty(stream, idx, shape[:-1], torch.float32)
+    rstd = _empty(stream, idx, shape[:-1], torch.float32)
+    st = lib.kda_layernorm_fwd(px, pw, pb, T, G, D, code, eps, _at(y, "y", dt, shape, idx),
+                               mean.data_ptr(), rstd.data_ptr(), handle)
     if st != KDA_OK:
         raise KdaError(st, "kda_layernorm_fwd")
     return y, mean, rstd
@@ -848,28 +870,28 @@ def kda_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rst
     a weight) and dbias (with bias=True), fp32 of the weight's shape (a bias
     without a weight: [D])."""
     lib = load_library()
-    dev, T, G, D, dt = _norm_sizes(x, weight)
-    _check(dy, "dy", dt, x.shape, dev)
-    _check(mean, "mean", torch.float32, x.shape[:-1], dev)
-    _check(rstd, "rstd", torch.float32, x.shape[:-1], dev)
-    shape = (D,)
+    idx, T, G, D, dt, code = _norm_sizes(x, weight)
+    shape = x.shape
+    px, pdy = _at(x, "x", dt, shape, idx), _at(dy, "dy", dt, shape, idx)
+    pm = _at(mean, "mean", torch.float32, shape[:-1], idx)
+    pr = _at(rstd, "rstd", torch.float32, shape[:-1], idx)
+    of = (G, D) if weight is not None and weight.dim() == 2 else (D,)
+    pw = _maybe(weight, "weight", torch.float32, of, idx)
+    handle = _stream_at(stream, idx)
+    if dx is None:
+        dx = _empty(stream, idx, shape, dt)
+    out = {"dx": dx}
+    pdw = pdb = None
     if weight is not None:
-        shape = (G, D) if weight.dim() == 2 else (D,)
-        _check(weight, "weight", torch.float32, shape, dev)
-    if dx is not None:
-        _check(dx, "dx", dt, x.shape, dev)
-    sums = weight is not None or bias
-    need = lib.kda_layernorm_bwd_workspace_size(T, G, D, _DTYPES[dt]) if sums else 0
-    with _on(stream):
-        out = {"dx": torch.empty_like(x) if dx is None else dx}
-        if weight is not None:
-            out["dweight"] = torch.empty(shape, dtype=torch.float32, device=dev)
-        if bias:
-            out["dbias"] = torch.empty(shape, dtype=torch.float32, device=dev)
-        ws, ws_bytes, _keep = _workspace(need, workspace, dev)
-    st = lib.kda_layernorm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), T, G, D,
-                               _DTYPES[dt], _ptr(out["dx"]), _ptr(out.get("dweight")),
-                               _ptr(out.get("dbias")), ws, ws_bytes, _stream_handle(stream))
+        out["dweight"] = _empty(stream, idx, of, torch.float32)
+        pdw = out["dweight"].data_ptr()
+    if bias:
+        out["dbias"] = _empty(stream, idx, of, torch.float32)
+        pdb = out["dbias"].data_ptr()
+    need = _size("kda_layernorm_bwd_workspace_size", T, G, D, code) if pdw or pdb else 0
+    ws, ws_bytes, _keep = _workspace(need, workspace, stream, idx)
+    st = lib.kda_layernorm_bwd(pdy, px, pm, pr, pw, T, G, D, code, _at(dx, "dx", dt, shape, idx), pdw, pdb,
+                               ws, ws_bytes, handle)
     if st != KDA_OK:
         raise KdaError(st, "kda_layernorm_bwd")
     return out

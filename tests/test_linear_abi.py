@@ -49,7 +49,7 @@ def test_prefill_refusals(lib):
     big = dict(T=T, Hk=1, H=H)
     assert _fwd(lib, **big) == WS and _fwd(lib, **big, ws=256, wsb=need - 1) == WS
     assert _fwd(lib, **big, ws=272, wsb=need) == WS
-    assert lib.kda_linear_chunk_fwd_workspace_size(1, 64, 2, 64, 0) == 0
+    assert lib.kda_linear_chunk_fwd_workspace_size(1, 64, 2, 128, 0) == 0
     assert lib.kda_linear_chunk_fwd_workspace_size(1, 1 << 16, 2, 48, 0) == 0
 
 
