@@ -2,6 +2,7 @@
 // positions and layer norm.  Included by kda_api.cu.
 #pragma once
 
+#include <algorithm>
 #include <cmath>
 
 namespace kda {
@@ -48,80 +49,89 @@ kda_status launch(const void *q, const void *k, const float *freq, Args a, bool 
 
 namespace ln {
 
-// The smallest row share that holds D values with kNV vectors a thread.
-#define KDA_LN_DISPATCH(D, V, NV, CALL)                                                    \
-    ((D) <= 2 * (V) * (NV)     ? CALL(2)                                                   \
-     : (D) <= 8 * (V) * (NV)   ? CALL(8)                                                   \
-     : (D) <= 32 * (V) * (NV)  ? CALL(32)                                                  \
-     : (D) <= 128 * (V) * (NV) ? CALL(128)                                                 \
-     : (D) <= 256 * (V) * (NV) ? CALL(256)                                                 \
-                               : CALL(512))
-
 constexpr int kMaxD = 8192;
 
+// The smallest row share that holds D values, and the values of a thread: 16 up to
+// 512, then 64 bytes of them.
 template <typename T>
-struct Wide;
-template <>
-struct Wide<__nv_bfloat16> { static constexpr int V = 8, NV = 2; };
-template <>
-struct Wide<float> { static constexpr int V = 4, NV = 4; };
+constexpr int long_per() { return 64 / (int)sizeof(T); }
+#define KDA_LN_DISPATCH(T, D, CALL)                         \
+    ((D) <= 32                   ? CALL(2, 16)              \
+     : (D) <= 128                ? CALL(8, 16)              \
+     : (D) <= 512                ? CALL(32, 16)             \
+     : (D) <= 64 * long_per<T>() ? CALL(64, long_per<T>())  \
+     : (D) <= 128 * long_per<T>() ? CALL(128, long_per<T>()) \
+     : (D) <= 256 * long_per<T>() ? CALL(256, long_per<T>()) \
+                                  : CALL(512, 16))
 
-template <typename T, int V, int kTpr, int kNV>
-kda_status fwd_at(const void *x, const float *w, const float *b, int64_t rows, int G, int D,
-                  float eps, void *y, float *mean, float *rstd, cudaStream_t s) {
-    const int64_t blocks = (rows + Block<kTpr>::kRows - 1) / Block<kTpr>::kRows;
-    if (blocks > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
-    fwd_kernel<T, V, kTpr, kNV><<<(unsigned)blocks, Block<kTpr>::kThreads, 0, s>>>(
-        (const T *)x, w, b, rows, G, D, eps, (T *)y, mean, rstd);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-}
-
-template <typename T, int V, int NV>
-kda_status fwd(const void *x, const float *w, const float *b, int64_t rows, int G, int D,
-               float eps, void *y, float *mean, float *rstd, cudaStream_t s) {
-#define KDA_LN_FWD(TPR) fwd_at<T, V, TPR, NV>(x, w, b, rows, G, D, eps, y, mean, rstd, s)
-    return KDA_LN_DISPATCH(D, V, NV, KDA_LN_FWD);
-#undef KDA_LN_FWD
-}
-
-// Threads that share a row, for the sizes of the gradient's grid.
-inline int row_share(int D, int per_thread) {
-#define KDA_LN_TPR(TPR) TPR
-    return KDA_LN_DISPATCH(D, per_thread, 1, KDA_LN_TPR);
+// Threads that share a row.
+inline int row_share(int D, kda_dtype dt) {
+#define KDA_LN_TPR(TPR, PER) TPR
+    return dt == KDA_BF16 ? KDA_LN_DISPATCH(__nv_bfloat16, D, KDA_LN_TPR) : KDA_LN_DISPATCH(float, D, KDA_LN_TPR);
 #undef KDA_LN_TPR
 }
 
-// Blocks along the tokens of a group: about four of 256 threads (two of 512) on
-// every SM over all groups.
-inline int bwd_blocks(int64_t tokens, int G, int tpr) {
+// How rows fall on blocks: gs groups of a block (the largest power of two that G
+// and the block's rows share), and blocks along the tokens, so that all groups
+// together have about `per_sm` blocks on every SM.
+struct Grid {
+    int gs, blocks;
+};
+inline Grid make_grid(int64_t tokens, int G, int tpr, int per_sm) {
     const int rows = tpr < 256 ? 256 / tpr : 1;
-    const int64_t most = (tokens + rows - 1) / rows;
-    int64_t want = (148 * (tpr > 256 ? 2 : 4) + G - 1) / G;
-    return (int)(want < most ? want : most < 1 ? 1 : most);
+    int gs = 1;
+    while (2 * gs <= rows && G % (2 * gs) == 0) gs *= 2;
+    const int ts = rows / gs;
+    const int64_t most = (tokens + ts - 1) / ts;
+    const int64_t want = std::max(148 * per_sm / (G / gs), 1);
+    return {gs, (int)(want < most ? want : most < 1 ? 1 : most)};
 }
+constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
 
-// Values of a row that one thread holds: 16 in every form.
-constexpr int kPerThread = 16;
-
-template <typename T, int V, int kTpr, int kNV>
-kda_status bwd_at(const void *dy, const void *x, const float *mean, const float *rstd,
-                  const float *w, int64_t tokens, int G, int D, void *dx, float *part, int blocks,
-                  cudaStream_t s) {
-    using B = Block<kTpr>;
-    static_assert(V * kNV == kPerThread, "row share");
-    const size_t smem = B::kRows > 1 && part ? (size_t)B::kRows * D * sizeof(float) : 0;
-    auto kern = bwd_kernel<T, V, kTpr, kNV>;
-    kern<<<dim3((unsigned)blocks, (unsigned)G), B::kThreads, smem, s>>>(
-        (const T *)dy, (const T *)x, mean, rstd, w, tokens, G, D, (T *)dx, part);
+template <typename T, int V, int kTpr, int kPer>
+kda_status fwd_at(const void *x, const float *w, const float *b, int64_t tokens, int G, int D,
+                  float eps, void *y, float *mean, float *rstd, cudaStream_t s) {
+    constexpr int kNV = kPer / V, kThreads = Block<kTpr>::kThreads;
+    const Grid g = make_grid(tokens, G, kTpr, kFwdPerSm);
+    auto kern = D == kTpr * V * kNV ? fwd_kernel<T, V, kTpr, kNV, true> : fwd_kernel<T, V, kTpr, kNV, false>;
+    const size_t smem = Feed<T, V, kNV, kThreads, 1>::kSmem;
+    if (!lin::set_smem(kern, smem)) return KDA_ERR_CUDA;
+    kern<<<dim3((unsigned)g.blocks, (unsigned)(G / g.gs)), kThreads, smem, s>>>(
+        (const T *)x, w, b, tokens, G, g.gs, D, eps, (T *)y, mean, rstd);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-template <typename T, int V, int NV>
+template <typename T, int V>
+kda_status fwd(const void *x, const float *w, const float *b, int64_t tokens, int G, int D,
+               float eps, void *y, float *mean, float *rstd, cudaStream_t s) {
+#define KDA_LN_FWD(TPR, PER) fwd_at<T, V, TPR, PER>(x, w, b, tokens, G, D, eps, y, mean, rstd, s)
+    return KDA_LN_DISPATCH(T, D, KDA_LN_FWD);
+#undef KDA_LN_FWD
+}
+
+template <typename T, int V, int kTpr, int kPer, bool kBias>
+kda_status bwd_at(const void *dy, const void *x, const float *mean, const float *rstd,
+                  const float *w, int64_t tokens, int G, int D, void *dx, float *part,
+                  cudaStream_t s) {
+    constexpr int kNV = kPer / V, kRows = Block<kTpr>::kRows, kThreads = Block<kTpr>::kThreads;
+    const Grid g = make_grid(tokens, G, kTpr, kBwdPerSm);
+    const size_t sums = kRows != g.gs && part ? (size_t)kRows * D * sizeof(float) : 0;
+    const size_t rows = Feed<T, V, kNV, kThreads, 2>::kSmem, smem = std::max(rows, sums);
+    auto kern = D == kTpr * V * kNV ? bwd_kernel<T, V, kTpr, kNV, true, kBias>
+                                    : bwd_kernel<T, V, kTpr, kNV, false, kBias>;
+    if (!lin::set_smem(kern, smem)) return KDA_ERR_CUDA;
+    kern<<<dim3((unsigned)g.blocks, (unsigned)(G / g.gs)), kThreads, smem, s>>>(
+        (const T *)dy, (const T *)x, mean, rstd, w, tokens, G, g.gs, D, (T *)dx, part);
+    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+template <typename T, int V>
 kda_status bwd(const void *dy, const void *x, const float *mean, const float *rstd, const float *w,
-               int64_t tokens, int G, int D, void *dx, float *part, int blocks, cudaStream_t s) {
-#define KDA_LN_BWD(TPR) \
-    bwd_at<T, V, TPR, NV>(dy, x, mean, rstd, w, tokens, G, D, dx, part, blocks, s)
-    return KDA_LN_DISPATCH(D, V, NV, KDA_LN_BWD);
+               int64_t tokens, int G, int D, void *dx, float *part, bool bias, cudaStream_t s) {
+#define KDA_LN_BWD(TPR, PER)                                                                   \
+    (bias ? bwd_at<T, V, TPR, PER, true>(dy, x, mean, rstd, w, tokens, G, D, dx, part, s)      \
+          : bwd_at<T, V, TPR, PER, false>(dy, x, mean, rstd, w, tokens, G, D, dx, part, s))
+    return KDA_LN_DISPATCH(T, D, KDA_LN_BWD);
 #undef KDA_LN_BWD
 }
 
@@ -240,18 +250,18 @@ extern "C" KDA_API kda_status kda_layernorm_fwd(const void *x, const float *weig
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     using namespace kda::ln;
     if (dt == KDA_BF16)
-        return D % 8 == 0
-                   ? fwd<__nv_bfloat16, 8, 2>(x, weight, bias, T * G, G, D, eps, y, mean, rstd, s)
-                   : fwd<__nv_bfloat16, 1, 16>(x, weight, bias, T * G, G, D, eps, y, mean, rstd, s);
-    return D % 4 == 0 ? fwd<float, 4, 4>(x, weight, bias, T * G, G, D, eps, y, mean, rstd, s)
-                      : fwd<float, 1, 16>(x, weight, bias, T * G, G, D, eps, y, mean, rstd, s);
+        return D % 8 == 0   ? fwd<__nv_bfloat16, 8>(x, weight, bias, T, G, D, eps, y, mean, rstd, s)
+               : D % 2 == 0 ? fwd<__nv_bfloat16, 2>(x, weight, bias, T, G, D, eps, y, mean, rstd, s)
+                            : fwd<__nv_bfloat16, 1>(x, weight, bias, T, G, D, eps, y, mean, rstd, s);
+    return D % 4 == 0 ? fwd<float, 4>(x, weight, bias, T, G, D, eps, y, mean, rstd, s)
+                      : fwd<float, 1>(x, weight, bias, T, G, D, eps, y, mean, rstd, s);
 }
 
 extern "C" KDA_API size_t kda_layernorm_bwd_workspace_size(int64_t T, int32_t G, int32_t D,
                                                            kda_dtype dt) {
     if (kda::ln::check(T, G, D, dt) != KDA_OK || T == 0) return 0;
-    const int blocks = kda::ln::bwd_blocks(T, G, kda::ln::row_share(D, kda::ln::kPerThread));
-    return (size_t)blocks * 2 * G * D * sizeof(float);
+    const kda::ln::Grid g = kda::ln::make_grid(T, G, kda::ln::row_share(D, dt), kda::ln::kBwdPerSm);
+    return (size_t)g.blocks * 2 * G * D * sizeof(float);
 }
 
 extern "C" KDA_API kda_status kda_layernorm_bwd(const void *dy, const void *x, const float *mean,
@@ -281,15 +291,16 @@ extern "C" KDA_API kda_status kda_layernorm_bwd(const void *dy, const void *x, c
         return KDA_ERR_WORKSPACE;
     float *part = sums ? (float *)workspace : nullptr;
     using namespace kda::ln;
-    const int blocks = bwd_blocks(T, G, row_share(D, kPerThread));
+    const int blocks = make_grid(T, G, row_share(D, dt), kBwdPerSm).blocks;
+    const bool b = dbias != nullptr;
     kda_status st;
     if (dt == KDA_BF16)
-        st = D % 8 == 0
-                 ? bwd<__nv_bfloat16, 8, 2>(dy, x, mean, rstd, weight, T, G, D, dx, part, blocks, s)
-                 : bwd<__nv_bfloat16, 1, 16>(dy, x, mean, rstd, weight, T, G, D, dx, part, blocks, s);
+        st = D % 8 == 0   ? bwd<__nv_bfloat16, 8>(dy, x, mean, rstd, weight, T, G, D, dx, part, b, s)
+             : D % 2 == 0 ? bwd<__nv_bfloat16, 2>(dy, x, mean, rstd, weight, T, G, D, dx, part, b, s)
+                          : bwd<__nv_bfloat16, 1>(dy, x, mean, rstd, weight, T, G, D, dx, part, b, s);
     else
-        st = D % 4 == 0 ? bwd<float, 4, 4>(dy, x, mean, rstd, weight, T, G, D, dx, part, blocks, s)
-                        : bwd<float, 1, 16>(dy, x, mean, rstd, weight, T, G, D, dx, part, blocks, s);
+        st = D % 4 == 0 ? bwd<float, 4>(dy, x, mean, rstd, weight, T, G, D, dx, part, b, s)
+                        : bwd<float, 1>(dy, x, mean, rstd, weight, T, G, D, dx, part, b, s);
     if (st != KDA_OK || !sums) return st;
     const int64_t n = (int64_t)G * D;
     weight_sum_kernel<<<dim3((unsigned)((n + 31) / 32), dbias != nullptr ? 2 : 1), 256, 0, s>>>(

@@ -156,6 +156,7 @@ inline bool ok16(const void *p) { return p == nullptr || aligned16(p); }
 
 template <typename K>
 inline bool set_smem(K kern, size_t bytes) {
+    if (bytes <= 40 * 1024) return true;               // 48 KB, static arrays included, need no asking
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
            cudaSuccess;
 }

@@ -48,6 +48,17 @@ struct Vec<T, 1> {
     static __device__ __forceinline__ void st(T *p, const float (&x)[1]) { IO<T>::st(p, x[0]); }
 };
 template <>
+struct Vec<__nv_bfloat16, 2> {
+    static __device__ __forceinline__ void ld(const __nv_bfloat16 *p, float (&x)[2]) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+        x[0] = __uint_as_float(w << 16);
+        x[1] = __uint_as_float(w & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void st(__nv_bfloat16 *p, const float (&x)[2]) {
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x[0], x[1]);
+    }
+};
+template <>
 struct Vec<float, 4> {
     static __device__ __forceinline__ void ld(const float *p, float (&x)[4]) {
         const float4 a = *reinterpret_cast<const float4 *>(p);
