@@ -574,31 +574,31 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             const float a = mode == kDirect ? direct_row_factor(d, row, p.scale) : d.y[row];
             __nv_bfloat16 *og = p.o + ((size_t)(sg.t0 + c * kTok + row) * p.H + h) * kD;
 #pragma unroll 1
-            for (int jb = 0; jb < 4; ++jb) {
-                uint32_t r[32];
-                tmem_ld32(tq + kColX + 32 * jb, r);
+            for (int jb = 0; jb < 2; ++jb) {           // 64 columns at once: two loads in flight
+                uint32_t r[2][32];
+                tmem_ld32(tq + kColX + 64 * jb, r[0]);
+                tmem_ld32(tq + kColX + 64 * jb + 32, r[1]);
                 tmem_wait_ld();
-                if (jb == 3) {
+                if (jb == 1) {
                     tc_fence_before();
                     arrive(&sm.x_free);
                     arrive(&sm.dec_free[c & 1]);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     uint4 y;
                     uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 x = fmul2(make_float2(__uint_as_float(r[8 * j + 2 * i]),
-                                                           __uint_as_float(r[8 * j + 2 * i + 1])),
+                        const float2 x = fmul2(make_float2(__uint_as_float(r[j >> 2][8 * (j & 3) + 2 * i]),
+                                                           __uint_as_float(r[j >> 2][8 * (j & 3) + 2 * i + 1])),
                                                make_float2(a, a));
                         yw[i] = pack_bf16(x.x, x.y);
                     }
                     if (whole_chunk)
-                        *reinterpret_cast<uint4 *>(st + (jb >> 1) * kHalf +
-                                                   sw128_off(row, 32 * (jb & 1) + 8 * j)) = y;
+                        *reinterpret_cast<uint4 *>(st + jb * kHalf + sw128_off(row, 8 * j)) = y;
                     else if (c * kTok + row < len)
-                        *reinterpret_cast<uint4 *>(og + 32 * jb + 8 * j) = y;
+                        *reinterpret_cast<uint4 *>(og + 64 * jb + 8 * j) = y;
                 }
             }
             fence_proxy_async_smem();
