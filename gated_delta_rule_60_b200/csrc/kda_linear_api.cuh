@@ -274,15 +274,17 @@ inline kda_status fwd_tensor(const Plan &p, const FwdArgs &a, cudaStream_t s) {
         tc::Params r = t;
         r.out = reinterpret_cast<float *>(a.ws);
         r.total = reinterpret_cast<float *>(a.ws + p.state_bytes);
-        if (!set_smem(tc::linear_sm100_kernel<true>, tc::kSmem)) return KDA_ERR_CUDA;
-        tc::linear_sm100_kernel<true><<<blocks, tc::kThreads, tc::kSmem, s>>>(mq, mk, mv, mo, r);
+        constexpr size_t smem = tc::smem_bytes<true>();
+        if (!set_smem(tc::linear_sm100_kernel<true>, smem)) return KDA_ERR_CUDA;
+        tc::linear_sm100_kernel<true><<<blocks, tc::kThreads, smem, s>>>(mq, mk, mv, mo, r);
         kda_status st = launched();
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, tc::kD, a.h0, r.total, r.out, s);
         if (st != KDA_OK) return st;
         t.ws = r.out;
     }
-    if (!set_smem(tc::linear_sm100_kernel<false>, tc::kSmem)) return KDA_ERR_CUDA;
-    tc::linear_sm100_kernel<false><<<blocks, tc::kThreads, tc::kSmem, s>>>(mq, mk, mv, mo, t);
+    constexpr size_t smem = tc::smem_bytes<false>();
+    if (!set_smem(tc::linear_sm100_kernel<false>, smem)) return KDA_ERR_CUDA;
+    tc::linear_sm100_kernel<false><<<blocks, tc::kThreads, smem, s>>>(mq, mk, mv, mo, t);
     return launched();
 }
 

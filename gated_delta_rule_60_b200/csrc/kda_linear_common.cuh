@@ -161,8 +161,8 @@ __device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, ui
 // segment's R, on return the state it starts from (forward) or the gradient of
 // the state it ends in (reverse).  Elementwise, so bound by memory: one read and
 // one write of each R.  grid (elements / 1024, H, N); a thread owns 4 elements
-// and prefetches the next segment's R before it needs it.
-constexpr int kScanThreads = 256;
+// and asks for the R of 8 segments at once.
+constexpr int kScanThreads = 256, kScanAhead = 8;
 
 template <bool kReverse>
 __global__ void __launch_bounds__(kScanThreads)
@@ -180,18 +180,27 @@ segment_scan_kernel(SegMap m, int H, int dd, const float *init, const float *__r
         if (init != nullptr)
             S = *reinterpret_cast<const float4 *>(init + ((size_t)n * H + h) * dd + e);
         const int step = kReverse ? -1 : 1;
-        int u = kReverse ? base + count - 1 : base;
-        // the last segment in scan order has no R: nothing starts from its end
-        float4 next = *reinterpret_cast<const float4 *>(ws + ((size_t)u * H + h) * dd + e);
-        for (int i = 0; i < count; ++i, u += step) {
-            const float4 R = next;
-            if (i + 2 < count)
-                next = *reinterpret_cast<const float4 *>(ws + ((size_t)(u + step) * H + h) * dd + e);
-            *reinterpret_cast<float4 *>(ws + ((size_t)u * H + h) * dd + e) = S;
-            if (i + 1 < count) {
-                const float a = total[(size_t)u * H + h];
-                S.x = fmaf(a, S.x, R.x); S.y = fmaf(a, S.y, R.y);
-                S.z = fmaf(a, S.z, R.z); S.w = fmaf(a, S.w, R.w);
+        const int first = kReverse ? base + count - 1 : base;
+        const size_t stride = (size_t)H * dd;
+        float *p = ws + ((size_t)first * H + h) * dd + e;
+        for (int i0 = 0; i0 < count; i0 += kScanAhead) {
+            float4 R[kScanAhead];
+            float a[kScanAhead];
+#pragma unroll
+            for (int i = 0; i < kScanAhead; ++i)       // nothing starts from the last one's end
+                if (i0 + i + 1 < count) {
+                    const int64_t k = (int64_t)(i0 + i) * step;
+                    R[i] = *reinterpret_cast<const float4 *>(p + k * (int64_t)stride);
+                    a[i] = total[(first + k) * H + h];
+                }
+#pragma unroll
+            for (int i = 0; i < kScanAhead; ++i) {
+                if (i0 + i >= count) break;
+                *reinterpret_cast<float4 *>(p + (int64_t)(i0 + i) * step * (int64_t)stride) = S;
+                if (i0 + i + 1 < count) {
+                    S.x = fmaf(a[i], S.x, R[i].x); S.y = fmaf(a[i], S.y, R[i].y);
+                    S.z = fmaf(a[i], S.z, R[i].z); S.w = fmaf(a[i], S.w, R[i].w);
+                }
             }
         }
     }

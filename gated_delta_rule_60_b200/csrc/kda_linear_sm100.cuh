@@ -45,12 +45,21 @@ namespace tc {
 
 using namespace kda::sm100;
 
-constexpr int kD = 128, kTok = 128, kThreads = 512, kStages = 2;
+constexpr int kD = 128, kTok = 128, kThreads = 512;
 constexpr uint32_t kTile = kTok * kD * 2;              // 32 KB; two halves of 64 channels
 constexpr uint32_t kHalf = kTile / 2;
-constexpr uint32_t kStageBytes = 3 * kTile;            // Q, K, V
-constexpr uint32_t kOffS = kStages * kStageBytes;      // S''
-constexpr uint32_t kOffSmall = kOffS + kTile;
+
+// Shared memory.  Outputs: two stages of Q, K, V, then S''.  States: three stages of
+// K and V (with two, the tiles of a chunk were asked for 1,400 cycles before they
+// were needed, less than a copy from L2 takes).
+template <bool kStates>
+struct Space {
+    static constexpr int kStages = kStates ? 3 : 2;
+    static constexpr uint32_t kStage = (kStates ? 2 : 3) * kTile;
+    static constexpr uint32_t kK = kStates ? 0 : kTile, kV = kK + kTile;   // in a stage; Q at 0
+    static constexpr uint32_t kS = kStages * kStage;
+    static constexpr uint32_t kSmall = kS + (kStates ? 0 : kTile);
+};
 
 // Tensor-memory columns.
 constexpr uint32_t kColX = 0, kColP = 128, kColD = 192, kColV = 320, kVBuf = 96, kVPart = 32;
@@ -71,6 +80,7 @@ struct __align__(16) Decay {
     int mode;
 };
 
+template <int kStages>
 struct Small {
     Decay dec[kStages];
     uint64_t full[kStages], dec_free[kStages];
@@ -82,8 +92,11 @@ struct Small {
     volatile int abort;
 };
 
-constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
-static_assert(kSmem <= 232448, "shared memory");
+template <bool kStates>
+constexpr uint32_t smem_bytes() {
+    return Space<kStates>::kSmall + (uint32_t)sizeof(Small<Space<kStates>::kStages>);
+}
+static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory");
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -96,7 +109,8 @@ __device__ __forceinline__ bool elect_one() {
 // at least where a poll returns at once.  The loop is kept short: sixteen warps
 // in six roles share the instruction caches.
 constexpr int kPolls = 1 << 18;
-__device__ __forceinline__ bool wait(Small &sm, uint64_t *bar, uint32_t parity) {
+template <typename S>
+__device__ __forceinline__ bool wait(S &sm, uint64_t *bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
 #pragma unroll 1
     for (int n = 0; n < kPolls; ++n) {
@@ -309,13 +323,17 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                     const Params p) {
     extern __shared__ __align__(1024) unsigned char sh[];
-    Small &sm = *reinterpret_cast<Small *>(sh + kOffSmall);
+    using Sp = Space<kStates>;
+    constexpr int kStages = Sp::kStages;
+    Small<kStages> &sm = *reinterpret_cast<Small<kStages> *>(sh + Sp::kSmall);
+    auto slot = [](int c) { return kStages == 2 ? c & 1 : c % kStages; };
+    auto phase = [](int c) { return kStages == 2 ? (c >> 1) & 1 : (c / kStages) & 1; };
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int h = blockIdx.x % p.H;
     int u = blockIdx.x / p.H;
     if (!kStates && blockIdx.x == 0) check_seqlens(p.m);
     if (p.m.cu != nullptr && p.m.units > 1 && p.m.units <= kThreads)
-        u = ranked_unit(p.m, u, reinterpret_cast<int *>(sh + kOffS));
+        u = ranked_unit(p.m, u, reinterpret_cast<int *>(sh));
     Segment sg;
     if (!find_segment(p.m, u, sg)) return;
     if (kStates && sg.s == sg.count - 1) return;
@@ -358,18 +376,18 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         // ------------------------------------------------------------ tiles
         auto load = [&](int c) {
             if (elect_one()) {
-                unsigned char *st = sh + (c & 1) * kStageBytes;
-                uint64_t *bar = &sm.full[c & 1];
+                unsigned char *st = sh + slot(c) * Sp::kStage;
+                uint64_t *bar = &sm.full[slot(c)];
                 const int t = t_first + c * kTok;
                 mbar_expect_tx(bar, kStates ? 2 * kTile : 3 * kTile);
-                tma_load_3d(st + kTile, &map_k, bar, 0, hk, t);
-                tma_load_3d(st + kTile + kHalf, &map_k, bar, 64, hk, t);
+                tma_load_3d(st + Sp::kK, &map_k, bar, 0, hk, t);
+                tma_load_3d(st + Sp::kK + kHalf, &map_k, bar, 64, hk, t);
                 if (!kStates) {
                     tma_load_3d(st, &map_q, bar, 0, hk, t);
                     tma_load_3d(st + kHalf, &map_q, bar, 64, hk, t);
                 }
-                tma_load_3d(st + 2 * kTile, &map_v, bar, 0, h, t);
-                tma_load_3d(st + 2 * kTile + kHalf, &map_v, bar, 64, h, t);
+                tma_load_3d(st + Sp::kV, &map_v, bar, 0, h, t);
+                tma_load_3d(st + Sp::kV + kHalf, &map_v, bar, 64, h, t);
             }
             __syncwarp();
         };
@@ -392,10 +410,10 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         int c = 0;
         for (; c < chunks; ++c) {
             if (!kStates) {
-                if (!wait(sm, &sm.staged[c & 1], (c >> 1) & 1)) break;
+                if (!wait(sm, &sm.staged[slot(c)], phase(c))) break;
                 if (len - c * kTok >= kTok) {
                     if (elect_one()) {
-                        const unsigned char *st = sh + (c & 1) * kStageBytes;
+                        const unsigned char *st = sh + slot(c) * Sp::kStage;
                         const int t = t_first + c * kTok;
                         tma_store_3d(&map_o, st, 0, h, t);
                         tma_store_3d(&map_o, st + kHalf, 64, h, t);
@@ -405,13 +423,13 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     __syncwarp();
                 }
             }
-            if (!wait(sm, &sm.k_free[c & 1], (c >> 1) & 1)) break;
+            if (!wait(sm, &sm.k_free[slot(c)], phase(c))) break;
             if (c + kStages < chunks) load(c + kStages);
             prefetch(c + kStages + 1);
         }
         if (c < chunks) {                              // gave up: let the copies in flight land
             const int issued = c + kStages < chunks ? c + kStages : chunks;
-            for (int i = c; i < issued; ++i) mbar_wait_drain(&sm.full[i & 1], (i >> 1) & 1, kWaitLimit);
+            for (int i = c; i < issued; ++i) mbar_wait_drain(&sm.full[slot(i)], phase(i), kWaitLimit);
         }
         if (elect_one()) bulk_wait_group<0>();
         __syncwarp();
@@ -419,14 +437,14 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         // ------------------------------------------- Q K^T, then P' V + Q S''
         constexpr uint32_t id_kk = idesc_bf16(128, 128, false, false);
         constexpr uint32_t id_kn = idesc_bf16(128, 128, false, true);
-        const uint64_t ds = sdesc(base + kOffS, kHalf, 1024, kLayoutSW128);
+        const uint64_t ds = sdesc(base + Sp::kS, kHalf, 1024, kLayoutSW128);
         int c = 0;
         for (; c < chunks; ++c) {
-            const uint32_t st = base + (c & 1) * kStageBytes;
+            const uint32_t st = base + slot(c) * Sp::kStage;
             const uint64_t dq = sdesc(st, kHalf, 1024, kLayoutSW128);
-            const uint64_t dk = sdesc(st + kTile, kHalf, 1024, kLayoutSW128);
-            const uint64_t dv = sdesc(st + 2 * kTile, kHalf, 1024, kLayoutSW128);
-            if (!wait(sm, &sm.full[c & 1], (c >> 1) & 1)) break;
+            const uint64_t dk = sdesc(st + Sp::kK, kHalf, 1024, kLayoutSW128);
+            const uint64_t dv = sdesc(st + Sp::kV, kHalf, 1024, kLayoutSW128);
+            if (!wait(sm, &sm.full[slot(c)], phase(c))) break;
             if (c > 0 && !wait(sm, &sm.x_free, (c - 1) & 1)) break;
             tc_fence_after();
             if (elect_one()) {
@@ -473,16 +491,16 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             LaneDecay d;
             decay_factors(d, g, p.scale);
             if (kStates) sum = add2(sum, d.end);
-            if (c >= kStages && !wait(sm, &sm.dec_free[c & 1], ((c >> 1) - 1) & 1)) break;
-            store_decay(sm.dec[c & 1], d);
-            arrive(&sm.full[c & 1]);
+            if (c >= kStages && !wait(sm, &sm.dec_free[slot(c)], phase(c - kStages))) break;
+            store_decay(sm.dec[slot(c)], d);
+            arrive(&sm.full[slot(c)]);
         }
         if (kStates && lane == 0) p.total[(size_t)u * p.H + h] = exp_sum(sum);
     } else if (warp == 3) {
         // ------------------------------------------------------------ V'^T K
         constexpr uint32_t id = idesc_bf16(128, 128, false, true);
         for (int c = 0; c < chunks; ++c) {
-            const uint64_t dk = sdesc(base + (c & 1) * kStageBytes + kTile, kHalf, 1024, kLayoutSW128);
+            const uint64_t dk = sdesc(base + slot(c) * Sp::kStage + Sp::kK, kHalf, 1024, kLayoutSW128);
             bool ok = true;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -502,7 +520,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                         tc_commit(&sm.v_free);
                     } else {
                         tc_commit(&sm.ds_full);
-                        tc_commit(&sm.k_free[c & 1]);
+                        tc_commit(&sm.k_free[slot(c)]);
                     }
                 }
                 __syncwarp();
@@ -523,8 +541,8 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         for (int i = 0; i < 16; ++i)
             below[i] = (lane >= 2 * i ? 0xffffu : 0u) | (lane >= 2 * i + 1 ? 0xffff0000u : 0u);
         for (int c = 0; c < chunks; ++c) {
-            const Decay &d = sm.dec[c & 1];
-            unsigned char *st = sh + (c & 1) * kStageBytes;
+            const Decay &d = sm.dec[slot(c)];
+            unsigned char *st = sh + slot(c) * Sp::kStage;
             const bool whole_chunk = len - c * kTok >= kTok;
             if (!wait(sm, &sm.d1_full, c & 1)) break;
             tc_fence_after();
@@ -582,7 +600,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 if (jb == 1) {
                     tc_fence_before();
                     arrive(&sm.x_free);
-                    arrive(&sm.dec_free[c & 1]);
+                    arrive(&sm.dec_free[slot(c)]);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -602,7 +620,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 }
             }
             fence_proxy_async_smem();
-            arrive(&sm.staged[c & 1]);
+            arrive(&sm.staged[slot(c)]);
         }
     } else if (warp >= 8) {
         // ------------------------------------------ V' and S (thread = value channel)
@@ -620,17 +638,17 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
 
         // one half (64 tokens) of V' of chunk c; this warp: 32 channels x 32 tokens
         auto produce = [&](int c, int hf) -> bool {
-            const Decay &d = sm.dec[c & 1];
-            unsigned char *st = sh + (c & 1) * kStageBytes;
+            const Decay &d = sm.dec[slot(c)];
+            unsigned char *st = sh + slot(c) * Sp::kStage;
             if (hf == 0) {
-                if (!wait(sm, &sm.full[c & 1], (c >> 1) & 1)) return false;
-                if (len - c * kTok < kTok) clear_tail(st + kTile, len - c * kTok);
+                if (!wait(sm, &sm.full[slot(c)], phase(c))) return false;
+                if (len - c * kTok < kTok) clear_tail(st + Sp::kK, len - c * kTok);
             }
             // the second half's buffer was free once the last chunk's V'^T K was done
             if (hf == 0 && c > 0 && !wait(sm, &sm.v_free, (c - 1) & 1)) return false;
             tc_fence_after();
             const int t0 = 64 * hf + 32 * side;        // tokens t0 .. t0 + 31
-            const uint32_t vt = base + (c & 1) * kStageBytes + 2 * kTile;
+            const uint32_t vt = base + slot(c) * Sp::kStage + Sp::kV;
             const uint32_t col = kColV + hf * kVBuf + 16 * side;
             // 16 tokens a step, both halves of the channels.  Matrices: (tokens 0-7,
             // channels 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
@@ -676,8 +694,8 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         };
         // S'' of chunk c into shared memory: row = value channel, this warp's key half
         auto publish = [&](int c) {
-            const float em = sm.dec[c & 1].em;
-            unsigned char *t = sh + kOffS + side * kHalf;
+            const float em = sm.dec[slot(c)].em;
+            unsigned char *t = sh + Sp::kS + side * kHalf;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 uint4 y;
@@ -703,7 +721,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 ok = wait(sm, &sm.ds_full, c & 1);
                 if (!ok) continue;
                 tc_fence_after();
-                const float gamma = sm.dec[c & 1].gamma;
+                const float gamma = sm.dec[slot(c)].gamma;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint32_t r[32];
@@ -712,7 +730,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     if (b == 1) {
                         tc_fence_before();
                         arrive(&sm.ds_free);
-                        arrive(&sm.dec_free[c & 1]);
+                        arrive(&sm.dec_free[slot(c)]);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
