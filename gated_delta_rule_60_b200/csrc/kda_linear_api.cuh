@@ -82,7 +82,7 @@ inline Costs fwd_costs(int32_t d, kda_dtype dt) {
 
 inline Costs bwd_costs(int32_t d, kda_dtype dt) {
     if (dt == KDA_BF16)
-        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 9.0 : 4.0, d == 128 ? 3.4 : 1.6};
+        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 20.0 : 6.0, d == 128 ? 2.4 : 2.4};
     return {kC, 148 * (d == 128 ? 1 : 2), d == 128 ? 16.0 : 8.0, d == 128 ? 6.0 : 3.0};
 }
 
@@ -247,6 +247,30 @@ kda_status fwd_mma(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     return launched();
 }
 
+inline tc::Params tensor_params(const Plan &p, const float *g, int per_token, int32_t Hk, int32_t H, float scale) {
+    tc::Params t = {};
+    t.g = g;
+    t.m = p.map;
+    t.per_token = per_token;
+    t.Hk = Hk;
+    t.H = H;
+    t.scale = scale;
+    return t;
+}
+
+// The segments' states on tcgen05: R and decays of `x` (Hk heads) and `y` (H heads).
+template <int kMode>
+kda_status tensor_states(const Plan &p, const CUtensorMap &x, const CUtensorMap &y, tc::Params t, float *out,
+                         float *total, cudaStream_t s) {
+    constexpr size_t smem = tc::smem_bytes<true>();
+    auto kern = tc::linear_sm100_kernel<kMode>;
+    t.out = out;
+    t.total = total;
+    if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
+    kern<<<(unsigned)((int64_t)p.map.units * t.H), tc::kThreads, smem, s>>>(x, x, y, y, t);
+    return launched();
+}
+
 // [T, heads, 128] maps; with no tokens no tile is copied, and the maps describe
 // a row of hT, which the caller has then given.
 inline kda_status fwd_tensor(const Plan &p, const FwdArgs &a, cudaStream_t s) {
@@ -257,34 +281,21 @@ inline kda_status fwd_tensor(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     if (!tc::make_map(&mq, base(a.q), a.Hk, rows) || !tc::make_map(&mk, base(a.k), a.Hk, rows) ||
         !tc::make_map(&mv, base(a.v), a.H, rows) || !tc::make_map(&mo, base(a.o), a.H, rows))
         return KDA_ERR_CUDA;
-    tc::Params t;
-    t.g = a.g;
+    tc::Params t = tensor_params(p, a.g, a.per_token, a.Hk, a.H, a.scale);
     t.h0 = a.h0;
-    t.ws = nullptr;
     t.out = a.hT;
-    t.total = nullptr;
     t.o = (__nv_bfloat16 *)a.o;
-    t.m = p.map;
-    t.per_token = a.per_token;
-    t.Hk = a.Hk;
-    t.H = a.H;
-    t.scale = a.scale;
-    const unsigned blocks = (unsigned)((int64_t)p.map.units * a.H);
     if (p.split) {
-        tc::Params r = t;
-        r.out = reinterpret_cast<float *>(a.ws);
-        r.total = reinterpret_cast<float *>(a.ws + p.state_bytes);
-        constexpr size_t smem = tc::smem_bytes<true>();
-        if (!set_smem(tc::linear_sm100_kernel<true>, smem)) return KDA_ERR_CUDA;
-        tc::linear_sm100_kernel<true><<<blocks, tc::kThreads, smem, s>>>(mq, mk, mv, mo, r);
-        kda_status st = launched();
-        if (st == KDA_OK) st = launch_scan<false>(p, a.H, tc::kD, a.h0, r.total, r.out, s);
+        float *states = reinterpret_cast<float *>(a.ws), *total = reinterpret_cast<float *>(a.ws + p.state_bytes);
+        kda_status st = tensor_states<tc::kForwardStates>(p, mk, mv, t, states, total, s);
+        if (st == KDA_OK) st = launch_scan<false>(p, a.H, tc::kD, a.h0, total, states, s);
         if (st != KDA_OK) return st;
-        t.ws = r.out;
+        t.ws = states;
     }
     constexpr size_t smem = tc::smem_bytes<false>();
-    if (!set_smem(tc::linear_sm100_kernel<false>, smem)) return KDA_ERR_CUDA;
-    tc::linear_sm100_kernel<false><<<blocks, tc::kThreads, smem, s>>>(mq, mk, mv, mo, t);
+    auto kern = tc::linear_sm100_kernel<tc::kOutputs>;
+    if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
+    kern<<<(unsigned)((int64_t)p.map.units * a.H), tc::kThreads, smem, s>>>(mq, mk, mv, mo, t);
     return launched();
 }
 
@@ -384,13 +395,24 @@ kda_status bwd_mma(const Plan &p, const BwdArgs &a, cudaStream_t s) {
     kda_status st = launch_factors(p, a.g, a.per_token, a.H, a.scale, b.factors, s);
     if (st != KDA_OK) return st;
     if (p.split) {
-        const size_t smem = sizeof(mm::StateSmem<D>);
-        auto fs = mm::state_kernel<D, false>;
-        auto rs = mm::state_kernel<D, true>;
-        if (!set_smem(fs, smem) || !set_smem(rs, smem)) return KDA_ERR_CUDA;
-        fs<<<grid, threads, smem, s>>>(k, v, b.factors, p.map, a.Hk, a.H, b.S, b.totS);
-        rs<<<grid, threads, smem, s>>>(q, dO, b.factors, p.map, a.Hk, a.H, b.E, b.totE);
-        st = launched();
+        if constexpr (D == tc::kD) {
+            CUtensorMap mq, mk, mv, md;
+            const int64_t T = p.map.T_tot;
+            if (!tc::make_map(&mq, q, a.Hk, T) || !tc::make_map(&mk, k, a.Hk, T) ||
+                !tc::make_map(&mv, v, a.H, T) || !tc::make_map(&md, dO, a.H, T))
+                return KDA_ERR_CUDA;
+            const tc::Params t = tensor_params(p, a.g, a.per_token, a.Hk, a.H, a.scale);
+            st = tensor_states<tc::kForwardStates>(p, mk, mv, t, b.S, b.totS, s);
+            if (st == KDA_OK) st = tensor_states<tc::kReverseStates>(p, mq, md, t, b.E, b.totE, s);
+        } else {
+            const size_t smem = sizeof(mm::StateSmem<D>);
+            auto fs = mm::state_kernel<D, false>;
+            auto rs = mm::state_kernel<D, true>;
+            if (!set_smem(fs, smem) || !set_smem(rs, smem)) return KDA_ERR_CUDA;
+            fs<<<grid, threads, smem, s>>>(k, v, b.factors, p.map, a.Hk, a.H, b.S, b.totS);
+            rs<<<grid, threads, smem, s>>>(q, dO, b.factors, p.map, a.Hk, a.H, b.E, b.totE);
+            st = launched();
+        }
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, b.totS, b.S, s);
         if (st == KDA_OK) st = launch_scan<true>(p, a.H, D, a.dhT, b.totE, b.E, s);
         if (st != KDA_OK) return st;
@@ -409,7 +431,7 @@ kda_status bwd_mma(const Plan &p, const BwdArgs &a, cudaStream_t s) {
     st = launched();
     if (st == KDA_OK && b.part) st = launch_group_sum<T>(b.part, a.dk, p.map.T_tot, a.Hk, a.H, D, s);
     if (st != KDA_OK) return st;
-    mm::decay_grad_kernel<<<dim3((unsigned)p.map.units, (unsigned)((a.H + 31) / 32)), 256, 0, s>>>(
+    mm::decay_grad_kernel<<<dim3((unsigned)p.map.units, (unsigned)((a.H + 31) / 32)), 32 * mm::kDecayWarps, 0, s>>>(
         b.term, b.anchor, a.per_token, p.map, a.H, a.dg, b.sums);
     st = launched();
     if (st == KDA_OK && !a.per_token) {

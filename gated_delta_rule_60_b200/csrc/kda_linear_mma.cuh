@@ -40,7 +40,7 @@ struct Shape {
 };
 
 struct __align__(16) Factors {
-    float hi[kTok], lo[kTok];          // b_i
+    float hi[kTok], lo[kTok];          // b_i / ln 2, a sum of two floats
     float row[kTok];                   // scale e^{b_i}
     float col[kTok];                   // e^{b_C - b_j}
     float gamma;                       // e^{b_C}
@@ -102,11 +102,16 @@ __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_grou
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *x, int64_t t, int L, int heads, int head) {
     using Sh = Shape<D>;
-    for (int e = threadIdx.x; e < kTok * (D / 8); e += Sh::kThreads) {
-        const int r = e / (D / 8), c = e % (D / 8) * 8;
-        const bool live = r < L;
-        cp_async16(dst + 2u * (r * Sh::kPitch + c),
-                   x + ((size_t)(t + (live ? r : 0)) * heads + head) * D + c, live);
+    // a thread keeps its column: rows r0, r0 + kStep, ...
+    constexpr int kStep = Sh::kThreads / (D / 8);
+    const int r0 = threadIdx.x / (D / 8), c = threadIdx.x % (D / 8) * 8;
+    const bf16 *base = x + ((size_t)t * heads + head) * D + c, *p = base + (size_t)r0 * heads * D;
+    const size_t step = (size_t)kStep * heads * D;
+    dst += 2u * (r0 * Sh::kPitch + c);
+#pragma unroll
+    for (int i = 0; i < kTok / kStep; ++i, p += step) {
+        const bool live = r0 + i * kStep < L;
+        cp_async16(dst + 2u * (i * kStep * Sh::kPitch), live ? p : base, live);
     }
 }
 
@@ -132,8 +137,11 @@ __device__ __forceinline__ void make_factors(Factors &f, float2 g, float scale) 
     const Sum2 b[2] = {b0, run};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        f.hi[2 * lane + i] = b[i].hi;
-        f.lo[2 * lane + i] = b[i].lo;
+        const float h2 = b[i].hi * kLog2e;             // log2 e = kLog2e + 1.9e-8
+        const Sum2 c = add2({h2, fmaf(b[i].hi, kLog2e, -h2)},
+                            {fmaf(b[i].lo, kLog2e, b[i].hi * 1.92596299e-8f), 0.f});
+        f.hi[2 * lane + i] = c.hi;
+        f.lo[2 * lane + i] = c.lo;
         f.row[2 * lane + i] = scale * exp_sum(b[i]);
         f.col[2 * lane + i] = exp_sum(add2(end, minus(b[i])));
     }
@@ -170,10 +178,11 @@ __device__ __forceinline__ void load_factors(Factors &f, const Factors *from) {
             cp_async16(sm100::smem_u32(&f) + 16 * e, reinterpret_cast<const char *>(from) + 16 * e, true);
 }
 
-// e^{b_i - b_j}
-__device__ __forceinline__ float spread(const Factors &f, int i, int j) {
-    return expf((f.hi[i] - f.hi[j]) + (f.lo[i] - f.lo[j]));
+// e^{b_i - b_j} from both sums
+__device__ __forceinline__ float spread(float2 i, float2 j) {
+    return sm100::ex2_approx((i.x - j.x) + (i.y - j.y));
 }
+__device__ __forceinline__ float2 sum_at(const Factors &f, int i) { return make_float2(f.hi[i], f.lo[i]); }
 
 // acc += (rows of X in registers) B^T, X = hi (+ mid + lo) terms of its
 // accumulators, B [64 tokens][D] in shared memory: out^T [16 rows][64 tokens].
@@ -189,15 +198,20 @@ __device__ __forceinline__ void state_times_tile(float (&acc)[8][4], const float
             if (kTerms == 3) split3(x, a[0][i], a[1][i], a[2][i]);
             else a[0][i] = sm100::pack_bf16(x.x, x.y);
         }
+        uint32_t r[2][2][4];
+        frag_b(b, Sh::kPitch, 0, 16 * k, r[0][0]);
+        frag_b(b, Sh::kPitch, 16, 16 * k, r[0][1]);
 #pragma unroll
-        for (int n = 0; n < 4; n += 2) {               // four accumulators between two uses of one
-            uint32_t r[2][4];
-            frag_b(b, Sh::kPitch, 16 * n, 16 * k, r[0]);
-            frag_b(b, Sh::kPitch, 16 * n + 16, 16 * k, r[1]);
+        for (int n = 0; n < 2; ++n) {                  // four accumulators between two uses of one
+            if (n == 0) {
+                frag_b(b, Sh::kPitch, 32, 16 * k, r[1][0]);
+                frag_b(b, Sh::kPitch, 48, 16 * k, r[1][1]);
+            }
 #pragma unroll
             for (int t = kTerms - 1; t >= 0; --t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma(acc[2 * n + i], a[t], r[i >> 1][2 * (i & 1)], r[i >> 1][2 * (i & 1) + 1]);
+                for (int i = 0; i < 4; ++i)
+                    mma(acc[4 * n + i], a[t], r[n][i >> 1][2 * (i & 1)], r[n][i >> 1][2 * (i & 1) + 1]);
         }
     }
 }
@@ -213,26 +227,30 @@ __device__ __forceinline__ void update_state(float (&X)[D / 8][4], uint32_t a_ti
     for (int n = 0; n < Sh::kN; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) add[n][i] = 0.f;
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < kTok / 16; ++k) {
-        uint32_t r[4], a[3][4];
+        constexpr int kB = Sh::kN >= 4 ? 2 : 1;        // pairs of n-tiles at once
+        constexpr int kG = Sh::kN / 2 / kB;
+        uint32_t r[4], a[3][4], b[2][kB][4];
         frag_at(a_tile, Sh::kPitch, r0, 16 * k, r);
+#pragma unroll
+        for (int i = 0; i < kB; ++i) frag_bt(b_tile, Sh::kPitch, 16 * i, 16 * k, b[0][i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = *reinterpret_cast<const float2 *>(c + 16 * k + 8 * (i >> 1) + 2 * (lane & 3));
             split3(sm100::fmul2(sm100::bf16x2_to_float2(r[i]), f), a[0][i], a[1][i], a[2][i]);
         }
-        constexpr int kB = Sh::kN >= 4 ? 2 : 1;        // pairs of n-tiles at once
 #pragma unroll
-        for (int n = 0; n < Sh::kN / 2; n += kB) {
-            uint32_t b[kB][4];
+        for (int n = 0; n < kG; ++n) {
+            if (n + 1 < kG)
 #pragma unroll
-            for (int i = 0; i < kB; ++i) frag_bt(b_tile, Sh::kPitch, 16 * (n + i), 16 * k, b[i]);
+                for (int i = 0; i < kB; ++i)
+                    frag_bt(b_tile, Sh::kPitch, 16 * (kB * (n + 1) + i), 16 * k, b[(n + 1) & 1][i]);
 #pragma unroll
             for (int t = 2; t >= 0; --t)
 #pragma unroll
                 for (int i = 0; i < 2 * kB; ++i)
-                    mma(add[2 * n + i], a[t], b[i >> 1][2 * (i & 1)], b[i >> 1][2 * (i & 1) + 1]);
+                    mma(add[2 * kB * n + i], a[t], b[n & 1][i >> 1][2 * (i & 1)], b[n & 1][i >> 1][2 * (i & 1) + 1]);
         }
     }
 #pragma unroll
@@ -434,15 +452,19 @@ out_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *_
             if (n0 > r0 + 15) continue;                // never read
             float c[4][4];
             unit_product<D>(c, tq, tk, r0, n0);
+            const float2 br[2] = {sum_at(f, r0 + (lane >> 2)), sum_at(f, r0 + (lane >> 2) + 8)};
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < 4; ++n) {
+                const int j = n0 + 8 * n + 2 * (lane & 3);
+                const float2 b0 = sum_at(f, j), b1 = sum_at(f, j + 1);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int r = r0 + (lane >> 2) + 8 * hf, j = n0 + 8 * n + 2 * (lane & 3);
-                    const float a = r >= j ? c[n][2 * hf] * spread(f, r, j) : 0.f;
-                    const float b = r >= j + 1 ? c[n][2 * hf + 1] * spread(f, r, j + 1) : 0.f;
+                    const int r = r0 + (lane >> 2) + 8 * hf;
+                    const float a = r >= j ? c[n][2 * hf] * spread(br[hf], b0) : 0.f;
+                    const float b = r >= j + 1 ? c[n][2 * hf + 1] * spread(br[hf], b1) : 0.f;
                     *reinterpret_cast<uint32_t *>(&sm.p[r * kPp + j]) = sm100::pack_bf16(a, b);
                 }
+            }
         }
         float acc[8][4];
         zero8(acc);
@@ -514,9 +536,11 @@ __device__ __forceinline__ void inside_chunk(GradSmem<D> &sm, int buf, const Fac
         unit_product<D>(c, tq, tk, r0, n0);
         unit_product<D>(d, td, tv, r0, n0);
         float sum[2] = {0.f, 0.f};
+        const float2 br[2] = {sum_at(f, r0 + (lane >> 2)), sum_at(f, r0 + (lane >> 2) + 8)};
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int j = n0 + 8 * n + 2 * (lane & 3);
+            const float2 bj[2] = {sum_at(f, j), sum_at(f, j + 1)};
             float col[2] = {0.f, 0.f};
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -524,10 +548,11 @@ __device__ __forceinline__ void inside_chunk(GradSmem<D> &sm, int buf, const Fac
                 float p[2], da[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float e = r >= j + i ? scale * spread(f, r, j + i) : 0.f;
-                    p[i] = r >= j + i ? c[n][2 * hf + i] * e : 0.f;
-                    da[i] = r >= j + i ? d[n][2 * hf + i] * e : 0.f;
-                    const float w = r >= j + i ? p[i] * d[n][2 * hf + i] : 0.f;
+                    const float e = scale * spread(br[hf], bj[i]);
+                    const bool in = r >= j + i;        // above the diagonal e may be anything
+                    p[i] = in ? c[n][2 * hf + i] * e : 0.f;
+                    da[i] = in ? d[n][2 * hf + i] * e : 0.f;
+                    const float w = in ? p[i] * d[n][2 * hf + i] : 0.f;
                     sum[hf] += w;
                     col[i] += w;
                 }
@@ -803,12 +828,13 @@ grad_kv_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf1
 }
 
 // dg_t = sum over the segment's tokens from t on of (x - y), plus <S_end, E_end>:
-// lanes are heads, the 8 warps of a block take an eighth of the tokens each (their
+// lanes are heads, the warps of a block take an equal share of the tokens each (their
 // totals first), sums in fp64.  With a constant decay the segment's sum goes out.
-__global__ void __launch_bounds__(256)
+constexpr int kDecayWarps = 32;
+__global__ void __launch_bounds__(32 * kDecayWarps)
 decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anchor, int per_token, SegMap m,
                   int H, float *__restrict__ dg, double *__restrict__ head_sum) {
-    __shared__ double total[8][33];
+    __shared__ double total[kDecayWarps][33];
     const int u = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int h = blockIdx.y * 32 + lane;
     Segment sg;
@@ -817,7 +843,7 @@ decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anc
         if (!per_token && warp == 0 && h < H) head_sum[(size_t)u * H + h] = 0.0;
         return;
     }
-    const int64_t len = sg.t1 - sg.t0, per = (len + 7) / 8;
+    const int64_t len = sg.t1 - sg.t0, per = (len + kDecayWarps - 1) / kDecayWarps;
     const int64_t a = sg.t0 + warp * per < sg.t1 ? sg.t0 + warp * per : sg.t1;
     const int64_t b = a + per < sg.t1 ? a + per : sg.t1;
     double s = 0.0;
@@ -828,7 +854,7 @@ decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anc
     total[warp][lane] = s;
     __syncthreads();
     s = h < H ? anchor[(size_t)u * H + h] : 0.0;
-    for (int i = 7; i > warp; --i) s += total[i][lane];
+    for (int i = kDecayWarps - 1; i > warp; --i) s += total[i][lane];
     double all = 0.0;
     if (h < H) {
 #pragma unroll 8
@@ -844,7 +870,7 @@ decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anc
     __syncthreads();
     if (warp == 0 && h < H) {
         all = 0.0;
-        for (int i = 0; i < 8; ++i) all += total[i][lane];
+        for (int i = 0; i < kDecayWarps; ++i) all += total[i][lane];
         head_sum[(size_t)u * H + h] = all;
     }
 }

@@ -222,6 +222,8 @@ struct LaneDecay {
     int level, mode;
 };
 
+// kReverse: x is r, and kv the level's own factor: x kv = scale e^{b_i}.
+template <bool kReverse>
 __device__ __forceinline__ void decay_factors(LaneDecay &d, const float (&g)[4], float scale) {
     const int lane = threadIdx.x & 31;
     Sum2 b[4];
@@ -267,10 +269,10 @@ __device__ __forceinline__ void decay_factors(LaneDecay &d, const float (&g)[4],
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const Sum2 t = add2(m, minus(b[i]));
-        d.x[i] = direct ? b[i].hi : exp_sum(t);
+        d.x[i] = direct ? b[i].hi : kReverse ? scale * exp_sum(minus(t)) : exp_sum(t);
         d.y[i] = direct ? b[i].lo : scale * exp_sum(minus(t));
     }
-    d.kv = direct ? 1.f : exp_sum(add2(d.end, minus(m)));
+    d.kv = direct ? 1.f : kReverse ? exp_sum(m) : exp_sum(add2(d.end, minus(m)));
     d.em = direct ? 1.f : exp_sum(m);
     d.gamma = exp_sum(d.end);
 }
@@ -316,12 +318,18 @@ __device__ __forceinline__ int ranked_unit(const SegMap &m, int rank, int *len) 
     return u;
 }
 
-// kStates: only S is wanted, from zero; R and the decay of the segment go out.
-template <bool kStates>
+// kOutputs: o and the final state.  kStates: only S is wanted, from zero; R and the
+// decay of the segment go out.  kReverse: the same for the gradient of the state,
+// R = sum_i scale e^{b_i} q_i dO_i^T, chunks last to first (map_k is that of q,
+// map_v that of dO).
+enum : int { kOutputs = 0, kForwardStates = 1, kReverseStates = 2 };
+
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
                     const Params p) {
+    constexpr bool kStates = kMode != kOutputs, kReverse = kMode == kReverseStates;
     extern __shared__ __align__(1024) unsigned char sh[];
     using Sp = Space<kStates>;
     constexpr int kStages = Sp::kStages;
@@ -336,7 +344,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         u = ranked_unit(p.m, u, reinterpret_cast<int *>(sh));
     Segment sg;
     if (!find_segment(p.m, u, sg)) return;
-    if (kStates && sg.s == sg.count - 1) return;
+    if (kStates && sg.s == (kReverse ? 0 : sg.count - 1)) return;
     const int len = (int)(sg.t1 - sg.t0);
     const int chunks = (len + kTok - 1) / kTok;
     const int hk = h / (p.H / p.Hk);
@@ -371,6 +379,8 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     const uint32_t tm = sm.tmem;
     const uint32_t base = smem_u32(sh);
     const int t_first = (int)sg.t0;                    // tokens stay below 2^31
+    // first token of the c-th chunk of the walk, counted from the segment's
+    auto first = [&](int c) { return (kReverse ? chunks - 1 - c : c) * kTok; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ tiles
@@ -378,7 +388,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             if (elect_one()) {
                 unsigned char *st = sh + slot(c) * Sp::kStage;
                 uint64_t *bar = &sm.full[slot(c)];
-                const int t = t_first + c * kTok;
+                const int t = t_first + first(c);
                 mbar_expect_tx(bar, kStates ? 2 * kTile : 3 * kTile);
                 tma_load_3d(st + Sp::kK, &map_k, bar, 0, hk, t);
                 tma_load_3d(st + Sp::kK + kHalf, &map_k, bar, 64, hk, t);
@@ -395,7 +405,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         // free is filled from there
         auto prefetch = [&](int c) {
             if (c < chunks && elect_one()) {
-                const int t = t_first + c * kTok;
+                const int t = t_first + first(c);
 #pragma unroll
                 for (int x = 0; x < kD; x += 64) {
                     tma_prefetch_3d(&map_k, x, hk, t);
@@ -414,7 +424,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 if (len - c * kTok >= kTok) {
                     if (elect_one()) {
                         const unsigned char *st = sh + slot(c) * Sp::kStage;
-                        const int t = t_first + c * kTok;
+                        const int t = t_first + first(c);
                         tma_store_3d(&map_o, st, 0, h, t);
                         tma_store_3d(&map_o, st + kHalf, 64, h, t);
                         bulk_commit_group();
@@ -477,7 +487,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         auto fetch = [&](int c, float (&x)[4]) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = c * kTok + 4 * lane + i;
+                const int t = first(c) + 4 * lane + i;
                 x[i] = t < len ? load_decay(p.g, p.per_token, sg.t0 + t, h, p.H) : 0.f;
             }
         };
@@ -489,7 +499,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             for (int i = 0; i < 4; ++i) g[i] = next[i];
             if (c + 1 < chunks) fetch(c + 1, next);
             LaneDecay d;
-            decay_factors(d, g, p.scale);
+            decay_factors<kReverse>(d, g, p.scale);
             if (kStates) sum = add2(sum, d.end);
             if (c >= kStages && !wait(sm, &sm.dec_free[slot(c)], phase(c - kStages))) break;
             store_decay(sm.dec[slot(c)], d);
@@ -642,7 +652,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             unsigned char *st = sh + slot(c) * Sp::kStage;
             if (hf == 0) {
                 if (!wait(sm, &sm.full[slot(c)], phase(c))) return false;
-                if (len - c * kTok < kTok) clear_tail(st + Sp::kK, len - c * kTok);
+                if (len - first(c) < kTok) clear_tail(st + Sp::kK, len - first(c));
             }
             // the second half's buffer was free once the last chunk's V'^T K was done
             if (hf == 0 && c > 0 && !wait(sm, &sm.v_free, (c - 1) & 1)) return false;
@@ -669,8 +679,10 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     if (d.mode != kDirect) {
                         f[i] = fmul2(dx, make_float2(kv, kv));
                     } else {
-                        f[i].x = __expf((d.end_hi - dx.x) + (d.end_lo - d.y[t]));
-                        f[i].y = __expf((d.end_hi - dx.y) + (d.end_lo - d.y[t + 1]));
+                        f[i].x = kReverse ? p.scale * __expf(dx.x + d.y[t])
+                                          : __expf((d.end_hi - dx.x) + (d.end_lo - d.y[t]));
+                        f[i].y = kReverse ? p.scale * __expf(dx.y + d.y[t + 1])
+                                          : __expf((d.end_hi - dx.y) + (d.end_lo - d.y[t + 1]));
                     }
                 }
 #pragma unroll
