@@ -22,8 +22,10 @@ struct Costs {
 // of segments that minimises the waves of both passes (the first over all segments
 // but the last).  Lengths that the host does not know: a slot's even share of the
 // tokens, which bounds what one long sequence can leave over; sequences below it
-// stay whole.  16 x 131,072 tokens: 9 segments 0.86 ms, unsplit 3.9 ms; 96 x 8,192:
-// unsplit 0.28 ms, any split adds a pass over all but the last segment.
+// stay whole.  16 x 131,072 tokens: 9 segments 0.73 ms, unsplit 3.9 ms; 96 x 8,192:
+// unsplit 0.25 ms, any split adds a pass over all but the last segment.  Half of
+// that share fits one packed batch better and another worse (gradient, 6 documents,
+// 16 heads: 678 -> 640 us; 2 documents, 8 heads: 344 -> 450 us).
 inline int64_t segment_length(int32_t N, bool equal, int64_t T_tot, int64_t chains, const Costs &c) {
     if (N <= 0 || T_tot <= 0) return kNoSplit;
     if (!equal && N > 1) {
@@ -52,6 +54,7 @@ struct Plan {
     bool split;
     size_t state_bytes, total_bytes;                   // of one direction
     size_t factor_bytes;                               // warp-level path: decay factors of the chunks
+    int bodies;                                        // T_tot / L: segments whose states are formed
 };
 
 inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, int32_t d, int64_t L,
@@ -63,6 +66,7 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
     p.map.L = L;
     p.map.units = (int)(T_tot / L + N);
     p.split = L != kNoSplit;
+    p.bodies = p.split ? (int)(T_tot / L) : 0;
     const size_t n = (size_t)p.map.units * H;
     p.state_bytes = p.split ? align256(n * d * d * sizeof(float)) : 0;
     p.total_bytes = p.split ? align256(n * sizeof(float)) : 0;
@@ -75,14 +79,14 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
 inline bool tensor_path(int32_t d, kda_dtype dt) { return d == 128 && dt == KDA_BF16; }
 
 inline Costs fwd_costs(int32_t d, kda_dtype dt) {
-    if (tensor_path(d, dt)) return {tc::kTok, 148, 1.9, 1.0};
+    if (tensor_path(d, dt)) return {tc::kTok, 148, 3.6, 2.1};
     if (dt == KDA_BF16) return {mm::kTok, 148 * (d == 64 ? 3 : 6), d == 64 ? 2.5 : 1.5, d == 64 ? 1.2 : 0.8};
     return {kC, 148 * (d >= 64 ? 2 : 4), 4.0, 1.5};
 }
 
 inline Costs bwd_costs(int32_t d, kda_dtype dt) {
     if (dt == KDA_BF16)
-        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 20.0 : 6.0, d == 128 ? 2.4 : 2.4};
+        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 20.0 : 6.0, 2.4};
     return {kC, 148 * (d == 128 ? 1 : 2), d == 128 ? 16.0 : 8.0, d == 128 ? 6.0 : 3.0};
 }
 
@@ -168,7 +172,7 @@ inline kda_status launch_scan(const Plan &p, int H, int d, const float *init, co
                               float *ws, cudaStream_t s) {
     const int dd = d * d;
     const dim3 grid((unsigned)((dd + 4 * kScanThreads - 1) / (4 * kScanThreads)), (unsigned)H,
-                    (unsigned)(p.map.N < 65535 ? p.map.N : 65535));
+                    (unsigned)(p.bodies < 65535 ? p.bodies : 65535));
     segment_scan_kernel<kReverse><<<grid, kScanThreads, 0, s>>>(p.map, H, dd, init, total, ws);
     return launched();
 }
@@ -194,8 +198,9 @@ kda_status fwd_simt(const Plan &p, const FwdArgs &a, cudaStream_t s) {
         total = reinterpret_cast<float *>(a.ws + p.state_bytes);
         auto kern = state_kernel<float, D, false>;
         const size_t smem = sizeof(StateSmem<D>);
+        const dim3 bodies((unsigned)p.bodies, grid.y, grid.z);
         if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-        kern<<<grid, kThreads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, states, total);
+        kern<<<bodies, kThreads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, states, total);
         kda_status st = launched();
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, total, states, s);
         if (st != KDA_OK) return st;
@@ -234,7 +239,7 @@ kda_status fwd_mma(const Plan &p, const FwdArgs &a, cudaStream_t s) {
         auto kern = mm::state_kernel<D, false>;
         const size_t smem = sizeof(mm::StateSmem<D>);
         if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-        kern<<<blocks, threads, smem, s>>>(k, v, f, p.map, a.Hk, a.H, states, total);
+        kern<<<(unsigned)((int64_t)p.bodies * a.H), threads, smem, s>>>(k, v, f, p.map, a.Hk, a.H, states, total);
         st = launched();
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, total, states, s);
         if (st != KDA_OK) return st;
@@ -267,7 +272,7 @@ kda_status tensor_states(const Plan &p, const CUtensorMap &x, const CUtensorMap 
     t.out = out;
     t.total = total;
     if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
-    kern<<<(unsigned)((int64_t)p.map.units * t.H), tc::kThreads, smem, s>>>(x, x, y, y, t);
+    kern<<<(unsigned)((int64_t)p.bodies * t.H), tc::kThreads, smem, s>>>(x, x, y, y, t);
     return launched();
 }
 
@@ -353,7 +358,7 @@ kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
     const float *q = (const float *)a.q, *k = (const float *)a.k, *v = (const float *)a.v, *dO = (const float *)a.dO;
     kda_status st = KDA_OK;
     if (p.split) {
-        const dim3 grid((unsigned)p.map.units, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
+        const dim3 grid((unsigned)p.bodies, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
         const size_t smem = sizeof(StateSmem<D>);
         auto fs = state_kernel<float, D, false>;
         auto rs = state_kernel<float, D, true>;
@@ -409,8 +414,9 @@ kda_status bwd_mma(const Plan &p, const BwdArgs &a, cudaStream_t s) {
             auto fs = mm::state_kernel<D, false>;
             auto rs = mm::state_kernel<D, true>;
             if (!set_smem(fs, smem) || !set_smem(rs, smem)) return KDA_ERR_CUDA;
-            fs<<<grid, threads, smem, s>>>(k, v, b.factors, p.map, a.Hk, a.H, b.S, b.totS);
-            rs<<<grid, threads, smem, s>>>(q, dO, b.factors, p.map, a.Hk, a.H, b.E, b.totE);
+            const unsigned bodies = (unsigned)((int64_t)p.bodies * a.H);
+            fs<<<bodies, threads, smem, s>>>(k, v, b.factors, p.map, a.Hk, a.H, b.S, b.totS);
+            rs<<<bodies, threads, smem, s>>>(q, dO, b.factors, p.map, a.Hk, a.H, b.E, b.totE);
             st = launched();
         }
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, b.totS, b.S, s);

@@ -78,6 +78,58 @@ __device__ __forceinline__ bool find_segment(const SegMap &m, int u, Segment &g)
     return true;
 }
 
+// Longest first.  Blocks start in index order, so with the units of a batch in
+// decreasing length the last to start are the short ones; each block ranks the
+// units itself (ties by index, so the ranks are a permutation).  Up to one unit a
+// thread; above that there are enough of them for their order not to matter.
+// len: kBlock + 1 words of shared memory that nobody uses yet.
+template <int kBlock>
+__device__ __forceinline__ int ranked_unit(const SegMap &m, int rank, int *len) {
+    if (m.cu == nullptr || m.units <= 1 || m.units > kBlock) return rank;
+    const int t = threadIdx.x;
+    if (t < m.units) {
+        Segment g;
+        len[t] = find_segment(m, t, g) ? (int)(g.t1 - g.t0) : -1;
+    }
+    if (t == 0) len[kBlock] = 0;
+    __syncthreads();
+    if (t < m.units) {
+        const int mine = len[t];
+        int r = 0;
+        for (int j = 0; j < m.units; ++j) r += (len[j] > mine) | ((len[j] == mine) & (j < t));
+        if (r == rank) len[kBlock] = t;
+    }
+    __syncthreads();
+    const int u = len[kBlock];
+    __syncthreads();
+    return u;
+}
+
+// The segments whose own states are wanted, all but one of each sequence (the last,
+// or in reverse the first), are numbered without gaps for short sequences:
+// segment i of them has the number start_n / L + i.  A sequence with any is longer
+// than L, so the numbers never meet, all lie below T_tot / L, and the owner of a
+// number is the last sequence that starts at or below it.  u: its unit.
+__device__ __forceinline__ bool find_body(const SegMap &m, int64_t j, bool reverse, Segment &g, int &u) {
+    int lo = 0, hi = m.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (seq_begin(m, mid) / m.L <= j) lo = mid;
+        else hi = mid - 1;
+    }
+    int64_t start, end;
+    int base;
+    g.n = lo;
+    if (!seq_segments(m, lo, start, end, base, g.count)) return false;
+    const int64_t i = j - start / m.L;
+    if (i < 0 || i >= g.count - 1) return false;
+    g.s = (int)i + (reverse ? 1 : 0);
+    u = base + g.s;
+    g.t0 = start + (int64_t)g.s * m.L;
+    g.t1 = g.t0 + m.L < end ? g.t0 + m.L : end;
+    return true;
+}
+
 // The whole of cu_seqlens is checked by one block (every other access relies on
 // the bounds of its own sequence alone): a descent between sequences that no
 // unit looks at is reported too.
@@ -160,8 +212,9 @@ __device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, ui
 // Scan over the segments of one (sequence, head): on entry ws[u][h] holds the
 // segment's R, on return the state it starts from (forward) or the gradient of
 // the state it ends in (reverse).  Elementwise, so bound by memory: one read and
-// one write of each R.  grid (elements / 1024, H, N); a thread owns 4 elements
-// and asks for the R of 8 segments at once.
+// one write of each R.  grid (elements / 1024, H, T_tot / L): a sequence of
+// several segments is the block's of the first, one of a single segment starts from
+// `init` itself.  A thread owns 4 elements and asks for the R of 8 segments at once.
 constexpr int kScanThreads = 256, kScanAhead = 8;
 
 template <bool kReverse>
@@ -171,11 +224,11 @@ segment_scan_kernel(SegMap m, int H, int dd, const float *init, const float *__r
     const int h = blockIdx.y;
     const int e = (blockIdx.x * kScanThreads + threadIdx.x) * 4;
     if (e >= dd) return;
-    for (int n = blockIdx.z; n < m.N; n += gridDim.z) {
-        int64_t start, end;
-        int base, count;
-        if (!seq_segments(m, n, start, end, base, count)) continue;
-        if (count == 1) continue;                      // starts from init itself
+    for (int64_t j = blockIdx.z; j < m.T_tot / m.L; j += gridDim.z) {
+        Segment g;
+        int base;
+        if (!find_body(m, j, false, g, base) || g.s != 0) continue;   // one block a sequence
+        const int n = g.n, count = g.count;
         float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
         if (init != nullptr)
             S = *reinterpret_cast<const float4 *>(init + ((size_t)n * H + h) * dd + e);

@@ -112,10 +112,10 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
     constexpr int W = Sm::kW;
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
-    const int u = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * W;
+    const int h = blockIdx.y, c0 = blockIdx.z * W;
+    int u;
     Segment sg;
-    if (!find_segment(m, u, sg)) return;
-    if (sg.s == (kReverse ? 0 : sg.count - 1)) return;
+    if (!find_body(m, blockIdx.x, kReverse, sg, u)) return;
     Tile<D, W> S;
     S.zero();
     double sum = 0.0;

@@ -293,31 +293,6 @@ __device__ __forceinline__ void store_decay(Decay &o, const LaneDecay &d) {
         o.mode = d.mode;
     }
 }
-
-// Longest first.  Blocks start in index order, so with the units of a batch in
-// decreasing length the last to start are the short ones; each block ranks the
-// units itself (ties by index, so the ranks are a permutation).  Up to one unit a
-// thread; above that there are enough of them for their order not to matter.
-__device__ __forceinline__ int ranked_unit(const SegMap &m, int rank, int *len) {
-    const int t = threadIdx.x;
-    if (t < m.units) {
-        Segment g;
-        len[t] = find_segment(m, t, g) ? (int)(g.t1 - g.t0) : -1;
-    }
-    if (t == 0) len[kThreads] = 0;
-    __syncthreads();
-    if (t < m.units) {
-        const int mine = len[t];
-        int r = 0;
-        for (int j = 0; j < m.units; ++j) r += (len[j] > mine) | ((len[j] == mine) & (j < t));
-        if (r == rank) len[kThreads] = t;
-    }
-    __syncthreads();
-    const int u = len[kThreads];
-    __syncthreads();
-    return u;
-}
-
 // kOutputs: o and the final state.  kStates: only S is wanted, from zero; R and the
 // decay of the segment go out.  kReverse: the same for the gradient of the state,
 // R = sum_i scale e^{b_i} q_i dO_i^T, chunks last to first (map_k is that of q,
@@ -340,11 +315,13 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     const int h = blockIdx.x % p.H;
     int u = blockIdx.x / p.H;
     if (!kStates && blockIdx.x == 0) check_seqlens(p.m);
-    if (p.m.cu != nullptr && p.m.units > 1 && p.m.units <= kThreads)
-        u = ranked_unit(p.m, u, reinterpret_cast<int *>(sh));
     Segment sg;
-    if (!find_segment(p.m, u, sg)) return;
-    if (kStates && sg.s == (kReverse ? 0 : sg.count - 1)) return;
+    if (kStates) {                                     // all of one length, but for sequence ends
+        if (!find_body(p.m, u, kReverse, sg, u)) return;
+    } else {
+        u = ranked_unit<kThreads>(p.m, u, reinterpret_cast<int *>(sh));
+        if (!find_segment(p.m, u, sg)) return;
+    }
     const int len = (int)(sg.t1 - sg.t0);
     const int chunks = (len + kTok - 1) / kTok;
     const int hk = h / (p.H / p.Hk);
