@@ -5,24 +5,23 @@
 namespace kda {
 namespace lin {
 
-constexpr int64_t kNoSplit = int64_t(1) << 40;         // segment length of "one segment each"
 
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // What a plan is made for: how many blocks run at once, and about what a chunk of
 // `tok` tokens costs a block in the main passes and in those that form the segments'
-// states (microseconds on a B200; only their ratios and the 8 us of two further
-// launches matter).
+// states, and what a segment costs the scan (microseconds on a B200; only their ratios
+// and the 8 us of two further launches matter).
 struct Costs {
     int tok, slots;
-    double main_us, state_us;
+    double main_us, state_us, scan_us;
 };
 
 // Tokens of a segment, for `chains` blocks per sequence.  Equal lengths: the number
 // of segments that minimises the waves of both passes (the first over all segments
 // but the last).  Lengths that the host does not know: a slot's even share of the
 // tokens, which bounds what one long sequence can leave over; sequences below it
-// stay whole.  16 x 131,072 tokens: 9 segments 0.73 ms, unsplit 3.9 ms; 96 x 8,192:
+// stay whole.  16 x 131,072 tokens: 9 segments 0.66 ms, 37 0.71 ms, unsplit 3.9 ms; 96 x 8,192:
 // unsplit 0.25 ms, any split adds a pass over all but the last segment.  Half of
 // that share fits one packed batch better and another worse (gradient, 6 documents,
 // 16 heads: 678 -> 640 us; 2 documents, 8 heads: 344 -> 450 us).
@@ -40,7 +39,8 @@ inline int64_t segment_length(int32_t N, bool equal, int64_t T_tot, int64_t chai
     int64_t L = kNoSplit;
     for (int64_t G = 2; G <= 64 && G * 4 <= chunks; ++G) {
         const int64_t per = (chunks + G - 1) / G;
-        const double t = (double)per * (waves(N * chains * G) * c.main_us + waves(N * chains * (G - 1)) * c.state_us) + 8.0;
+        const double t = (double)per * (waves(N * chains * G) * c.main_us + waves(N * chains * (G - 1)) * c.state_us) +
+                         8.0 + (double)(N * chains * G) * c.scan_us;
         if (t < best) {
             best = t;
             L = per * c.tok;
@@ -65,6 +65,7 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
     p.map.T_tot = T_tot;
     p.map.L = L;
     p.map.units = (int)(T_tot / L + N);
+    p.map.per = (int)(T_tot / N);
     p.split = L != kNoSplit;
     p.bodies = p.split ? (int)(T_tot / L) : 0;
     const size_t n = (size_t)p.map.units * H;
@@ -78,16 +79,19 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
 // instructions, fp32 on CUDA cores.
 inline bool tensor_path(int32_t d, kda_dtype dt) { return d == 128 && dt == KDA_BF16; }
 
+// The scan reads and writes a state of every segment, at about 3.5 TB/s.
+inline double scan_us(int32_t d) { return 8.0 * d * d / 3.5e6; }
+
 inline Costs fwd_costs(int32_t d, kda_dtype dt) {
-    if (tensor_path(d, dt)) return {tc::kTok, 148, 3.6, 2.1};
-    if (dt == KDA_BF16) return {mm::kTok, 148 * (d == 64 ? 3 : 6), d == 64 ? 2.5 : 1.5, d == 64 ? 1.2 : 0.8};
-    return {kC, 148 * (d >= 64 ? 2 : 4), 4.0, 1.5};
+    if (tensor_path(d, dt)) return {tc::kTok, 148, 3.6, 2.1, scan_us(d)};
+    if (dt == KDA_BF16) return {mm::kTok, 148 * (d == 64 ? 3 : 6), d == 64 ? 2.5 : 1.5, d == 64 ? 1.2 : 0.8, scan_us(d)};
+    return {kC, 148 * (d >= 64 ? 2 : 4), 4.0, 1.5, scan_us(d)};
 }
 
 inline Costs bwd_costs(int32_t d, kda_dtype dt) {
     if (dt == KDA_BF16)
-        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 20.0 : 6.0, 2.4};
-    return {kC, 148 * (d == 128 ? 1 : 2), d == 128 ? 16.0 : 8.0, d == 128 ? 6.0 : 3.0};
+        return {mm::kTok, 148 * (d == 128 ? 1 : d == 64 ? 2 : 3), d == 128 ? 20.0 : 6.0, 2.4, 2 * scan_us(d)};
+    return {kC, 148 * (d == 128 ? 1 : 2), d == 128 ? 16.0 : 8.0, d == 128 ? 6.0 : 3.0, 2 * scan_us(d)};
 }
 
 // The workspace query does not know whether cu_seqlens is given: with several
@@ -171,8 +175,9 @@ template <bool kReverse>
 inline kda_status launch_scan(const Plan &p, int H, int d, const float *init, const float *total,
                               float *ws, cudaStream_t s) {
     const int dd = d * d;
+    const int64_t z = scan_blocks(p.map);
     const dim3 grid((unsigned)((dd + 4 * kScanThreads - 1) / (4 * kScanThreads)), (unsigned)H,
-                    (unsigned)(p.bodies < 65535 ? p.bodies : 65535));
+                    (unsigned)(z < 65535 ? z : 65535));
     segment_scan_kernel<kReverse><<<grid, kScanThreads, 0, s>>>(p.map, H, dd, init, total, ws);
     return launched();
 }

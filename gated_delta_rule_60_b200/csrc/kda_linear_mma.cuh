@@ -850,7 +850,7 @@ grad_kv_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf1
 // dg_t = sum over the segment's tokens from t on of (x - y), plus <S_end, E_end>:
 // lanes are heads, the warps of a block take an equal share of the tokens each (their
 // totals first), sums in fp64.  With a constant decay the segment's sum goes out.
-constexpr int kDecayWarps = 32;
+constexpr int kDecayWarps = 32, kDecayAhead = 16;
 __global__ void __launch_bounds__(32 * kDecayWarps)
 decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anchor, int per_token, SegMap m,
                   int H, float *__restrict__ dg, double *__restrict__ head_sum) {
@@ -863,27 +863,35 @@ decay_grad_kernel(const float *__restrict__ term, const double *__restrict__ anc
         if (!per_token && warp == 0 && h < H) head_sum[(size_t)u * H + h] = 0.0;
         return;
     }
-    const int64_t len = sg.t1 - sg.t0, per = (len + kDecayWarps - 1) / kDecayWarps;
-    const int64_t a = sg.t0 + warp * per < sg.t1 ? sg.t0 + warp * per : sg.t1;
-    const int64_t b = a + per < sg.t1 ? a + per : sg.t1;
+    const int len = (int)(sg.t1 - sg.t0), per = (len + kDecayWarps - 1) / kDecayWarps;
+    const int a = min(warp * per, len), b = min(a + per, len);
+    // the shares' terms from the last token on, sixteen loads at a time
+    auto walk = [&](auto visit) {
+        if (h >= H) return;
+        const float *p = term + (size_t)sg.t0 * H + h;
+        for (int t = b - 1; t >= a; t -= kDecayAhead) {
+            float x[kDecayAhead];
+#pragma unroll
+            for (int i = 0; i < kDecayAhead; ++i)
+                if (t - i >= a) x[i] = p[(size_t)(t - i) * H];
+#pragma unroll
+            for (int i = 0; i < kDecayAhead; ++i)
+                if (t - i >= a) visit(t - i, (double)x[i]);
+        }
+    };
     double s = 0.0;
-    if (h < H) {
-#pragma unroll 8
-        for (int64_t t = b - 1; t >= a; --t) s += (double)term[(size_t)t * H + h];
-    }
+    walk([&](int, double x) { s += x; });
     total[warp][lane] = s;
     __syncthreads();
     s = h < H ? anchor[(size_t)u * H + h] : 0.0;
     for (int i = kDecayWarps - 1; i > warp; --i) s += total[i][lane];
     double all = 0.0;
-    if (h < H) {
-#pragma unroll 8
-        for (int64_t t = b - 1; t >= a; --t) {
-            s += (double)term[(size_t)t * H + h];
-            if (per_token) dg[(size_t)t * H + h] = (float)s;
-            all += s;
-        }
-    }
+    float *out = dg + (size_t)(per_token ? sg.t0 : 0) * H + h;
+    walk([&](int t, double x) {
+        s += x;
+        if (per_token) out[(size_t)t * H] = (float)s;
+        all += s;
+    });
     if (per_token) return;
     __syncthreads();
     total[warp][lane] = all;
