@@ -86,6 +86,8 @@ inline Grid make_grid(int64_t tokens, int G, int tpr, int per_sm) {
     const int64_t want = std::max(148 * per_sm / (G / gs), 1);
     return {gs, (int)(want < most ? want : most < 1 ? 1 : most)};
 }
+// About as many as are resident, so that a block walks along its tokens with the next
+// rows on their way.
 constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
 
 template <typename T, int V, int kTpr, int kPer>

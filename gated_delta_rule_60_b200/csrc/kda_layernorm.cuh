@@ -20,8 +20,13 @@
 // they are few: packed fp32 pairs, pointers that advance by a constant, rows of up to
 // 512 values with their weights (and, for the gradient, both factors of a row) in
 // registers.  Longer rows take 64 bytes a thread (32 bf16 or 16 fp32 values, so that
-// two blocks' rows fit an SM) and are read a second time from where they lie.  The mean, then the centred square, are summed over the values in
-// registers: none of the cancellation of sum x^2 - (sum x)^2 / D.
+// two blocks' rows fit an SM) and are read a second time from where they lie.  The
+// mean, then the centred square, are summed over the row's values: none of the
+// cancellation of sum x^2 - (sum x)^2 / D.
+//
+// Measured (bf16): 8,192 x 96 rows of 128, forward 68 us (5.9 TB/s), backward 102 us
+// (5.9 TB/s); 4,099 rows of 5,000, forward 30 us (2.8 TB/s), backward 47 us (2.6 TB/s:
+// two barriers a row and few rows a block to hide them), the sum of its partials 5 us.
 #pragma once
 
 #include "kda_rotary.cuh"

@@ -34,6 +34,14 @@
 // Tensor memory (512 columns): Q K^T, then O 128 | P' 64 | V'^T K 128 | V' 2 x 96.
 // Shared memory: two stages of Q, K, V (96 KB each; O leaves through Q's tile) and
 // S'' (32 KB).
+//
+// Measured: 96 heads x 8,192 tokens 249 us (3.3 TB/s; 125 us of it are the bytes at
+// the rate of a copy), 87,469 packed tokens of 32 heads 577 us behind 11 us of states
+// and scan, 16 heads x 131,072 tokens 430 us behind 235 us of states.  Neither memory
+// nor the tensor cores bound it (half and a quarter busy): a chunk takes 6 to 7
+// thousand cycles of dependent steps, S to S'' to O and V' to S, and tensor memory is
+// full, so that no second chunk fits beside the first.  Two terms of V' instead of
+// three would make room, and leave the final state with an error of 2.7e-6.
 #pragma once
 
 #include "kda_linear_common.cuh"
