@@ -31,8 +31,10 @@ namespace lin {
 
 constexpr int kC = 32;                 // tokens of a chunk
 constexpr int kThreads = 256;
+constexpr int kPad = 4;                // floats behind a row in shared memory
 
-// A register tile of an M x N product over 256 threads: lanes run along N.
+// A register tile of an M x N product over 256 threads: lanes run along N, a thread's
+// rows are neighbours.
 template <int M, int N>
 struct Tile {
     static constexpr int kNT = N < 32 ? N : 32;
@@ -40,7 +42,7 @@ struct Tile {
     static constexpr int kI = M / kRows, kJ = N / kNT;
     static_assert(M % kRows == 0 && N % kNT == 0, "tile");
     float v[kI][kJ];
-    static __device__ __forceinline__ int m(int i) { return threadIdx.x / kNT + i * kRows; }
+    static __device__ __forceinline__ int m(int i) { return threadIdx.x / kNT * kI + i; }
     static __device__ __forceinline__ int n(int j) { return threadIdx.x % kNT + j * kNT; }
     __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -48,20 +50,60 @@ struct Tile {
 #pragma unroll
             for (int j = 0; j < kJ; ++j) v[i][j] = 0.f;
     }
-    // v += A B, A(m, k) = A[m lda + k] (or A[k lda + m] if TA), B alike.
+    // v += A B, A(m, k) = A[m lda + k] (or A[k lda + m] if TA), B alike, one k after
+    // the other.  Four k at a time: along k both operands are read as 16 bytes (A by
+    // all lanes of a row at once, B without bank conflicts, since rows are 4 floats
+    // apart modulo the banks), and so are a thread's rows of A if TA.
     template <int K, bool TA, bool TB>
     __device__ __forceinline__ void mac(const float *A, int lda, const float *B, int ldb) {
-#pragma unroll 4
-        for (int k = 0; k < K; ++k) {
-            float a[kI], b[kJ];
+        constexpr int kV = kI % 4 == 0 ? 4 : kI % 2 == 0 ? 2 : 1;
+        A += TA ? m(0) : m(0) * lda;
+        B += TB ? n(0) * ldb : n(0);
+#pragma unroll 2
+        for (int k = 0; k < K; k += 4) {
+            float b[4][kJ];
 #pragma unroll
-            for (int i = 0; i < kI; ++i) a[i] = TA ? A[k * lda + m(i)] : A[m(i) * lda + k];
+            for (int j = 0; j < kJ; ++j) {
+                if (TB) {
+                    const float4 x = *reinterpret_cast<const float4 *>(B + j * kNT * ldb + k);
+                    b[0][j] = x.x; b[1][j] = x.y; b[2][j] = x.z; b[3][j] = x.w;
+                } else {
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) b[j] = TB ? B[n(j) * ldb + k] : B[k * ldb + n(j)];
+                    for (int i = 0; i < 4; ++i) b[i][j] = B[(k + i) * ldb + j * kNT];
+                }
+            }
+            if (TA) {
 #pragma unroll
-            for (int i = 0; i < kI; ++i)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) v[i][j] = fmaf(a[i], b[j], v[i][j]);
+                    for (int i = 0; i < kI; i += kV) {
+                        float a[kV];
+                        const float *p = A + (k + c) * lda + i;
+                        if constexpr (kV == 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(p);
+                            a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
+                        } else if constexpr (kV == 2) {
+                            const float2 x = *reinterpret_cast<const float2 *>(p);
+                            a[0] = x.x; a[1] = x.y;
+                        } else {
+                            a[0] = *p;
+                        }
+#pragma unroll
+                        for (int r = 0; r < kV; ++r)
+#pragma unroll
+                            for (int j = 0; j < kJ; ++j) v[i + r][j] = fmaf(a[r], b[c][j], v[i + r][j]);
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kI; ++i) {
+                    const float4 x = *reinterpret_cast<const float4 *>(A + i * lda + k);
+                    const float a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < kJ; ++j) v[i][j] = fmaf(a[c], b[c][j], v[i][j]);
+                }
+            }
         }
     }
 };
@@ -79,10 +121,13 @@ __device__ __forceinline__ float row_sum(float x) {
 template <typename T, int W>
 __device__ __forceinline__ void load_tile(float *dst, const T *x, int64_t t0, int len, int heads,
                                           int head, int D, int c0) {
-    for (int e = threadIdx.x; e < kC * W; e += kThreads) {
-        const int r = e / W, c = e % W;
-        dst[r * (W + 1) + c] =
-            r < len ? IO<T>::ld(x + ((size_t)(t0 + r) * heads + head) * D + c0 + c) : 0.f;
+    static_assert(sizeof(T) == sizeof(float), "copied as fp32");
+    for (int e = threadIdx.x; e < kC * W / 4; e += kThreads) {
+        const int r = e / (W / 4), c = e % (W / 4) * 4;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < len)
+            y = *reinterpret_cast<const float4 *>(x + ((size_t)(t0 + r) * heads + head) * D + c0 + c);
+        *reinterpret_cast<float4 *>(dst + r * (W + kPad) + c) = y;
     }
 }
 
@@ -102,7 +147,7 @@ __device__ __forceinline__ void chunk_decays(double *b, const float *g, int per_
 template <int D>
 struct StateSmem {
     static constexpr int kW = D < 64 ? D : 64;         // value columns of a block
-    float x[kC * (D + 1)], y[kC * (kW + 1)];
+    float x[kC * (D + kPad)], y[kC * (kW + kPad)];
     double b[kC];
 };
 
@@ -136,7 +181,7 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
         sum += tot;
         for (int e = threadIdx.x; e < kC * W; e += kThreads) {
             const int r = e / W;
-            sm.y[r * (W + 1) + e % W] *=
+            sm.y[r * (W + kPad) + e % W] *=
                 kReverse ? scale * expf((float)sm.b[r]) : expf((float)(tot - sm.b[r]));
         }
         const float a = expf((float)tot);
@@ -145,7 +190,7 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
 #pragma unroll
             for (int j = 0; j < S.kJ; ++j) S.v[i][j] *= a;
         __syncthreads();
-        S.template mac<kC, true, false>(sm.x, D + 1, sm.y, W + 1);
+        S.template mac<kC, true, false>(sm.x, D + kPad, sm.y, W + kPad);
     }
     float *out = ws + ((size_t)u * H + h) * D * D + c0;
 #pragma unroll
@@ -159,8 +204,8 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
 template <int D>
 struct OutSmem {
     static constexpr int kW = D < 64 ? D : 64;
-    float S[D * (kW + 1)];
-    float q[kC * (D + 1)], k[kC * (D + 1)], v[kC * (kW + 1)], P[kC * (kC + 1)];
+    float S[D * (kW + kPad)];
+    float q[kC * (D + kPad)], k[kC * (D + kPad)], v[kC * (kW + kPad)], P[kC * (kC + kPad)];
     double b[kC];
 };
 
@@ -187,7 +232,7 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
 #pragma unroll
         for (int j = 0; j < S.kJ; ++j) {
             S.v[i][j] = from != nullptr ? from[(size_t)S.m(i) * D + c0 + S.n(j)] : 0.f;
-            sm.S[S.m(i) * (W + 1) + S.n(j)] = S.v[i][j];
+            sm.S[S.m(i) * (W + kPad) + S.n(j)] = S.v[i][j];
         }
     for (int64_t t = sg.t0; t < sg.t1; t += kC) {
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
@@ -199,17 +244,17 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
         __syncthreads();
         Tile<kC, kC> P;
         P.zero();
-        P.template mac<D, false, true>(sm.q, D + 1, sm.k, D + 1);
+        P.template mac<D, false, true>(sm.q, D + kPad, sm.k, D + kPad);
 #pragma unroll
         for (int i = 0; i < P.kI; ++i)
 #pragma unroll
             for (int j = 0; j < P.kJ; ++j) {
                 const int r = P.m(i), c = P.n(j);
-                sm.P[r * (kC + 1) + c] = r >= c ? P.v[i][j] * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
+                sm.P[r * (kC + kPad) + c] = r >= c ? P.v[i][j] * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
             }
         Tile<kC, W> O;
         O.zero();
-        O.template mac<D, false, false>(sm.q, D + 1, sm.S, W + 1);
+        O.template mac<D, false, false>(sm.q, D + kPad, sm.S, W + kPad);
 #pragma unroll
         for (int i = 0; i < O.kI; ++i) {
             const float a = expf((float)sm.b[O.m(i)]);
@@ -217,7 +262,7 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
             for (int j = 0; j < O.kJ; ++j) O.v[i][j] *= a;
         }
         __syncthreads();
-        O.template mac<kC, false, false>(sm.P, kC + 1, sm.v, W + 1);
+        O.template mac<kC, false, false>(sm.P, kC + kPad, sm.v, W + kPad);
 #pragma unroll
         for (int i = 0; i < O.kI; ++i)
             if (O.m(i) < L)
@@ -227,18 +272,18 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
         __syncthreads();
         const double tot = sm.b[kC - 1];
         for (int e = threadIdx.x; e < kC * W; e += kThreads)
-            sm.v[e / W * (W + 1) + e % W] *= expf((float)(tot - sm.b[e / W]));
+            sm.v[e / W * (W + kPad) + e % W] *= expf((float)(tot - sm.b[e / W]));
         const float a = expf((float)tot);
 #pragma unroll
         for (int i = 0; i < S.kI; ++i)
 #pragma unroll
             for (int j = 0; j < S.kJ; ++j) S.v[i][j] *= a;
         __syncthreads();
-        S.template mac<kC, true, false>(sm.k, D + 1, sm.v, W + 1);
+        S.template mac<kC, true, false>(sm.k, D + kPad, sm.v, W + kPad);
 #pragma unroll
         for (int i = 0; i < S.kI; ++i)
 #pragma unroll
-            for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (W + 1) + S.n(j)] = S.v[i][j];
+            for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (W + kPad) + S.n(j)] = S.v[i][j];
     }
     if (hT != nullptr && sg.s == sg.count - 1) {
         float *out = hT + ((size_t)sg.n * H + h) * D * D + c0;
@@ -252,9 +297,9 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
 // ------------------------------------------------------------- gradient
 template <int D>
 struct GradSmem {
-    float S[D * (D + 1)];                              // S (dQ) or E (dK, dV)
-    float q[kC * (D + 1)], k[kC * (D + 1)], v[kC * (D + 1)], dO[kC * (D + 1)];
-    float P[kC * (kC + 1)], A[kC * (kC + 1)];
+    float S[D * (D + kPad)];                              // S (dQ) or E (dK, dV)
+    float q[kC * (D + kPad)], k[kC * (D + kPad)], v[kC * (D + kPad)], dO[kC * (D + kPad)];
+    float P[kC * (kC + kPad)], A[kC * (kC + kPad)];
     double b[kC];
     float r[kC];
     double red[kThreads / 32];
@@ -275,8 +320,8 @@ __device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T 
     Tile<kC, kC> P, dP;
     P.zero();
     dP.zero();
-    P.template mac<D, false, true>(sm.q, D + 1, sm.k, D + 1);
-    dP.template mac<D, false, true>(sm.dO, D + 1, sm.v, D + 1);
+    P.template mac<D, false, true>(sm.q, D + kPad, sm.k, D + kPad);
+    dP.template mac<D, false, true>(sm.dO, D + kPad, sm.v, D + kPad);
 #pragma unroll
     for (int i = 0; i < P.kI; ++i)
 #pragma unroll
@@ -284,8 +329,8 @@ __device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T 
             const int r = P.m(i), c = P.n(j);
             const float e = r >= c ? scale * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
             const float p = P.v[i][j] * e;
-            sm.P[r * (kC + 1) + c] = r >= c ? (kW ? p * dP.v[i][j] : p) : 0.f;
-            sm.A[r * (kC + 1) + c] = r >= c ? dP.v[i][j] * e : 0.f;
+            sm.P[r * (kC + kPad) + c] = r >= c ? (kW ? p * dP.v[i][j] : p) : 0.f;
+            sm.A[r * (kC + kPad) + c] = r >= c ? dP.v[i][j] * e : 0.f;
         }
 }
 
@@ -321,7 +366,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 #pragma unroll
         for (int j = 0; j < S.kJ; ++j) {
             S.v[i][j] = from != nullptr ? from[(size_t)S.m(i) * D + S.n(j)] : 0.f;
-            sm.S[S.m(i) * (D + 1) + S.n(j)] = S.v[i][j];
+            sm.S[S.m(i) * (D + kPad) + S.n(j)] = S.v[i][j];
         }
     for (int64_t t = sg.t0; t < sg.t1; t += kC) {
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
@@ -329,7 +374,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
         grad_chunk<T, D, true>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
         Tile<kC, D> X;                                 // dO S^T
         X.zero();
-        X.template mac<D, false, true>(sm.dO, D + 1, sm.S, D + 1);
+        X.template mac<D, false, true>(sm.dO, D + kPad, sm.S, D + kPad);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < X.kI; ++i) {
@@ -339,12 +384,12 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 #pragma unroll
             for (int j = 0; j < X.kJ; ++j) {
                 X.v[i][j] *= a;
-                s = fmaf(X.v[i][j], sm.q[r * (D + 1) + X.n(j)], s);
+                s = fmaf(X.v[i][j], sm.q[r * (D + kPad) + X.n(j)], s);
             }
             s = row_sum<X.kNT>(s);
             if (threadIdx.x % X.kNT == 0) sm.r[r] = s;
         }
-        X.template mac<kC, false, false>(sm.A, kC + 1, sm.k, D + 1);
+        X.template mac<kC, false, false>(sm.A, kC + kPad, sm.k, D + kPad);
 #pragma unroll
         for (int i = 0; i < X.kI; ++i)
             if (X.m(i) < L)
@@ -355,7 +400,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                 }
         const double tot = sm.b[kC - 1];
         for (int e = threadIdx.x; e < kC * D; e += kThreads)
-            sm.v[e / D * (D + 1) + e % D] *= expf((float)(tot - sm.b[e / D]));
+            sm.v[e / D * (D + kPad) + e % D] *= expf((float)(tot - sm.b[e / D]));
         const float a = expf((float)tot);
 #pragma unroll
         for (int i = 0; i < S.kI; ++i)
@@ -365,14 +410,14 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
         if (threadIdx.x < L) {
             float s = sm.r[threadIdx.x];
             for (int c = 0; c < kC; ++c)
-                s += sm.P[threadIdx.x * (kC + 1) + c] - sm.P[c * (kC + 1) + threadIdx.x];
+                s += sm.P[threadIdx.x * (kC + kPad) + c] - sm.P[c * (kC + kPad) + threadIdx.x];
             term[(size_t)(t + threadIdx.x) * H + h] = s;
         }
-        S.template mac<kC, true, false>(sm.k, D + 1, sm.v, D + 1);
+        S.template mac<kC, true, false>(sm.k, D + kPad, sm.v, D + kPad);
 #pragma unroll
         for (int i = 0; i < S.kI; ++i)
 #pragma unroll
-            for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (D + 1) + S.n(j)] = S.v[i][j];
+            for (int j = 0; j < S.kJ; ++j) sm.S[S.m(i) * (D + kPad) + S.n(j)] = S.v[i][j];
     }
     const float *to = wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
     double s = 0.0;
@@ -419,7 +464,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
 #pragma unroll
         for (int j = 0; j < E.kJ; ++j) {
             E.v[i][j] = from != nullptr ? from[(size_t)E.m(i) * D + E.n(j)] : 0.f;
-            sm.S[E.m(i) * (D + 1) + E.n(j)] = E.v[i][j];
+            sm.S[E.m(i) * (D + kPad) + E.n(j)] = E.v[i][j];
         }
     double carry = anchor[(size_t)u * H + h], sum = 0.0;   // warp 0
     const int64_t chunks = (sg.t1 - sg.t0 + kC - 1) / kC;
@@ -431,7 +476,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
         const double tot = sm.b[kC - 1];
         Tile<kC, D> X;                                 // V E^T
         X.zero();
-        X.template mac<D, false, true>(sm.v, D + 1, sm.S, D + 1);
+        X.template mac<D, false, true>(sm.v, D + kPad, sm.S, D + kPad);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < X.kI; ++i) {
@@ -441,12 +486,12 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
 #pragma unroll
             for (int j = 0; j < X.kJ; ++j) {
                 X.v[i][j] *= a;
-                s = fmaf(X.v[i][j], sm.k[r * (D + 1) + X.n(j)], s);
+                s = fmaf(X.v[i][j], sm.k[r * (D + kPad) + X.n(j)], s);
             }
             s = row_sum<X.kNT>(s);
             if (threadIdx.x % X.kNT == 0) sm.r[r] = s;
         }
-        X.template mac<kC, true, false>(sm.A, kC + 1, sm.q, D + 1);
+        X.template mac<kC, true, false>(sm.A, kC + kPad, sm.q, D + kPad);
 #pragma unroll
         for (int i = 0; i < X.kI; ++i)
             if (X.m(i) < L)
@@ -456,14 +501,14 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
                     store_shared(dk, part, row * D + X.n(j), X.v[i][j]);
                 }
         X.zero();                                      // K E
-        X.template mac<D, false, false>(sm.k, D + 1, sm.S, D + 1);
+        X.template mac<D, false, false>(sm.k, D + kPad, sm.S, D + kPad);
 #pragma unroll
         for (int i = 0; i < X.kI; ++i) {
             const float a = expf((float)(tot - sm.b[X.m(i)]));
 #pragma unroll
             for (int j = 0; j < X.kJ; ++j) X.v[i][j] *= a;
         }
-        X.template mac<kC, true, false>(sm.P, kC + 1, sm.dO, D + 1);
+        X.template mac<kC, true, false>(sm.P, kC + kPad, sm.dO, D + kPad);
 #pragma unroll
         for (int i = 0; i < X.kI; ++i)
             if (X.m(i) < L)
@@ -472,7 +517,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
                     IO<T>::st(dv + ((size_t)(t + X.m(i)) * H + h) * D + X.n(j), X.v[i][j]);
         __syncthreads();
         for (int e = threadIdx.x; e < kC * D; e += kThreads)
-            sm.dO[e / D * (D + 1) + e % D] *= scale * expf((float)sm.b[e / D]);
+            sm.dO[e / D * (D + kPad) + e % D] *= scale * expf((float)sm.b[e / D]);
         if (threadIdx.x < 32) {                        // sums from the chunk's end
             const int i = threadIdx.x, r = 31 - i;
             double x = 0.0;
@@ -490,11 +535,11 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
 #pragma unroll
             for (int j = 0; j < E.kJ; ++j) E.v[i][j] *= a;
         __syncthreads();
-        E.template mac<kC, true, false>(sm.q, D + 1, sm.dO, D + 1);
+        E.template mac<kC, true, false>(sm.q, D + kPad, sm.dO, D + kPad);
 #pragma unroll
         for (int i = 0; i < E.kI; ++i)
 #pragma unroll
-            for (int j = 0; j < E.kJ; ++j) sm.S[E.m(i) * (D + 1) + E.n(j)] = E.v[i][j];
+            for (int j = 0; j < E.kJ; ++j) sm.S[E.m(i) * (D + kPad) + E.n(j)] = E.v[i][j];
     }
     if (!per_token && threadIdx.x < 32) {
 #pragma unroll
