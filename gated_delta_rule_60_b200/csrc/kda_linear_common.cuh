@@ -201,6 +201,14 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t addr, uint32_t (&r)[4]) 
                  : "memory");
 }
 
+// 16 bytes to shared memory, zeros (and nothing read) if not live
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // x = hi + mid + lo in bf16 pairs, each the leading 8 bits of what is left: cut,
 // not rounded, so that a part costs a byte permute instead of a conversion.  What
 // is left over is below 2^-24 of x.

@@ -95,13 +95,6 @@ __device__ __forceinline__ void frag_bt(uint32_t x, int pitch, int n0, int k0, u
     ldmatrix_trans(x + 2u * ((k0 + (l & 15)) * pitch + n0 + 8 * (l >> 4)), r);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-
 // 64 token rows of one head; rows behind L become zero (and are not read).
 template <int D>
 __device__ __forceinline__ void load_tile(uint32_t dst, const bf16 *x, int64_t t, int L, int heads, int head) {

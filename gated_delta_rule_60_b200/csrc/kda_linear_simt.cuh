@@ -124,20 +124,33 @@ __device__ __forceinline__ void load_tile(float *dst, const T *x, int64_t t0, in
     static_assert(sizeof(T) == sizeof(float), "copied as fp32");
     for (int e = threadIdx.x; e < kC * W / 4; e += kThreads) {
         const int r = e / (W / 4), c = e % (W / 4) * 4;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < len)
-            y = *reinterpret_cast<const float4 *>(x + ((size_t)(t0 + r) * heads + head) * D + c0 + c);
-        *reinterpret_cast<float4 *>(dst + r * (W + kPad) + c) = y;
+        const size_t row = t0 + (r < len ? r : 0);
+        cp_async16(sm100::smem_u32(dst + r * (W + kPad) + c), x + (row * heads + head) * D + c0 + c, r < len);
     }
 }
 
-// Decay sums of a chunk by warp 0: b_i in fp64 (b[i]), total b[kC - 1].
-__device__ __forceinline__ void chunk_decays(double *b, const float *g, int per_token, int64_t t0,
+// The decays of a chunk, by warp 0: sums b_i in fp64, and the factors e^{b_i} and
+// e^{b_C - b_i} of its rows.
+struct Decays {
+    double b[kC], tot;
+    float row[kC], col[kC];
+};
+__device__ __forceinline__ void chunk_decays(Decays &d, const float *g, int per_token, int64_t t0,
                                              int len, int h, int H) {
     if (threadIdx.x < 32) {
         const int i = threadIdx.x;
-        b[i] = warp_scan(i < len ? (double)load_decay(g, per_token, t0 + i, h, H) : 0.0);
+        const double b = warp_scan(i < len ? (double)load_decay(g, per_token, t0 + i, h, H) : 0.0);
+        const double tot = __shfl_sync(0xffffffffu, b, 31);
+        d.b[i] = b;
+        d.row[i] = expf((float)b);
+        d.col[i] = expf((float)(tot - b));
+        if (i == 0) d.tot = tot;
     }
+}
+// What the chunk's loads and decays are waited for with.
+__device__ __forceinline__ void chunk_ready() {
+    cp_wait_all();
+    __syncthreads();
 }
 
 // ------------------------------------------------------- segment states
@@ -148,7 +161,7 @@ template <int D>
 struct StateSmem {
     static constexpr int kW = D < 64 ? D : 64;         // value columns of a block
     float x[kC * (D + kPad)], y[kC * (kW + kPad)];
-    double b[kC];
+    Decays d;
 };
 
 template <typename T, int D, bool kReverse>
@@ -175,14 +188,14 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
         __syncthreads();
         load_tile<T, D>(sm.x, x, t, L, Hk, h / (H / Hk), D, 0);
         load_tile<T, W>(sm.y, y, t, L, H, h, D, c0);
-        chunk_decays(sm.b, g, per_token, t, L, h, H);
-        __syncthreads();
-        const double tot = sm.b[kC - 1];
+        chunk_decays(sm.d, g, per_token, t, L, h, H);
+        chunk_ready();
+        const double tot = sm.d.tot;
         sum += tot;
         for (int e = threadIdx.x; e < kC * W; e += kThreads) {
             const int r = e / W;
             sm.y[r * (W + kPad) + e % W] *=
-                kReverse ? scale * expf((float)sm.b[r]) : expf((float)(tot - sm.b[r]));
+                kReverse ? scale * sm.d.row[r] : sm.d.col[r];
         }
         const float a = expf((float)tot);
 #pragma unroll
@@ -206,7 +219,7 @@ struct OutSmem {
     static constexpr int kW = D < 64 ? D : 64;
     float S[D * (kW + kPad)];
     float q[kC * (D + kPad)], k[kC * (D + kPad)], v[kC * (kW + kPad)], P[kC * (kC + kPad)];
-    double b[kC];
+    Decays d;
 };
 
 // grid (units, H, D / kW): value columns are independent, so a head is split
@@ -240,8 +253,8 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
         load_tile<T, D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
         load_tile<T, D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
         load_tile<T, W>(sm.v, v, t, L, H, h, D, c0);
-        chunk_decays(sm.b, g, per_token, t, L, h, H);
-        __syncthreads();
+        chunk_decays(sm.d, g, per_token, t, L, h, H);
+        chunk_ready();
         Tile<kC, kC> P;
         P.zero();
         P.template mac<D, false, true>(sm.q, D + kPad, sm.k, D + kPad);
@@ -250,14 +263,14 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
 #pragma unroll
             for (int j = 0; j < P.kJ; ++j) {
                 const int r = P.m(i), c = P.n(j);
-                sm.P[r * (kC + kPad) + c] = r >= c ? P.v[i][j] * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
+                sm.P[r * (kC + kPad) + c] = r >= c ? P.v[i][j] * expf((float)(sm.d.b[r] - sm.d.b[c])) : 0.f;
             }
         Tile<kC, W> O;
         O.zero();
         O.template mac<D, false, false>(sm.q, D + kPad, sm.S, W + kPad);
 #pragma unroll
         for (int i = 0; i < O.kI; ++i) {
-            const float a = expf((float)sm.b[O.m(i)]);
+            const float a = sm.d.row[O.m(i)];
 #pragma unroll
             for (int j = 0; j < O.kJ; ++j) O.v[i][j] *= a;
         }
@@ -270,9 +283,9 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
                 for (int j = 0; j < O.kJ; ++j)
                     IO<T>::st(o + ((size_t)(t + O.m(i)) * H + h) * D + c0 + O.n(j), O.v[i][j] * scale);
         __syncthreads();
-        const double tot = sm.b[kC - 1];
+        const double tot = sm.d.tot;
         for (int e = threadIdx.x; e < kC * W; e += kThreads)
-            sm.v[e / W * (W + kPad) + e % W] *= expf((float)(tot - sm.b[e / W]));
+            sm.v[e / W * (W + kPad) + e % W] *= sm.d.col[e / W];
         const float a = expf((float)tot);
 #pragma unroll
         for (int i = 0; i < S.kI; ++i)
@@ -300,7 +313,7 @@ struct GradSmem {
     float S[D * (D + kPad)];                              // S (dQ) or E (dK, dV)
     float q[kC * (D + kPad)], k[kC * (D + kPad)], v[kC * (D + kPad)], dO[kC * (D + kPad)];
     float P[kC * (kC + kPad)], A[kC * (kC + kPad)];
-    double b[kC];
+    Decays d;
     float r[kC];
     double red[kThreads / 32];
 };
@@ -315,8 +328,8 @@ __device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T 
     load_tile<T, D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
     load_tile<T, D>(sm.v, v, t, L, H, h, D, 0);
     load_tile<T, D>(sm.dO, dO, t, L, H, h, D, 0);
-    chunk_decays(sm.b, g, per_token, t, L, h, H);
-    __syncthreads();
+    chunk_decays(sm.d, g, per_token, t, L, h, H);
+    chunk_ready();
     Tile<kC, kC> P, dP;
     P.zero();
     dP.zero();
@@ -327,7 +340,7 @@ __device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T 
 #pragma unroll
         for (int j = 0; j < P.kJ; ++j) {
             const int r = P.m(i), c = P.n(j);
-            const float e = r >= c ? scale * expf((float)(sm.b[r] - sm.b[c])) : 0.f;
+            const float e = r >= c ? scale * expf((float)(sm.d.b[r] - sm.d.b[c])) : 0.f;
             const float p = P.v[i][j] * e;
             sm.P[r * (kC + kPad) + c] = r >= c ? (kW ? p * dP.v[i][j] : p) : 0.f;
             sm.A[r * (kC + kPad) + c] = r >= c ? dP.v[i][j] * e : 0.f;
@@ -379,7 +392,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 #pragma unroll
         for (int i = 0; i < X.kI; ++i) {
             const int r = X.m(i);
-            const float a = scale * expf((float)sm.b[r]);
+            const float a = scale * sm.d.row[r];
             float s = 0.f;
 #pragma unroll
             for (int j = 0; j < X.kJ; ++j) {
@@ -398,9 +411,9 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
                     const size_t row = (size_t)(t + X.m(i)) * H + h;
                     store_shared(dq, part, row * D + X.n(j), X.v[i][j]);
                 }
-        const double tot = sm.b[kC - 1];
+        const double tot = sm.d.tot;
         for (int e = threadIdx.x; e < kC * D; e += kThreads)
-            sm.v[e / D * (D + kPad) + e % D] *= expf((float)(tot - sm.b[e / D]));
+            sm.v[e / D * (D + kPad) + e % D] *= sm.d.col[e / D];
         const float a = expf((float)tot);
 #pragma unroll
         for (int i = 0; i < S.kI; ++i)
@@ -473,7 +486,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
         __syncthreads();
         grad_chunk<T, D, false>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
-        const double tot = sm.b[kC - 1];
+        const double tot = sm.d.tot;
         Tile<kC, D> X;                                 // V E^T
         X.zero();
         X.template mac<D, false, true>(sm.v, D + kPad, sm.S, D + kPad);
@@ -481,7 +494,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
 #pragma unroll
         for (int i = 0; i < X.kI; ++i) {
             const int r = X.m(i);
-            const float a = expf((float)(tot - sm.b[r]));
+            const float a = sm.d.col[r];
             float s = 0.f;
 #pragma unroll
             for (int j = 0; j < X.kJ; ++j) {
@@ -504,7 +517,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
         X.template mac<D, false, false>(sm.k, D + kPad, sm.S, D + kPad);
 #pragma unroll
         for (int i = 0; i < X.kI; ++i) {
-            const float a = expf((float)(tot - sm.b[X.m(i)]));
+            const float a = sm.d.col[X.m(i)];
 #pragma unroll
             for (int j = 0; j < X.kJ; ++j) X.v[i][j] *= a;
         }
@@ -517,7 +530,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
                     IO<T>::st(dv + ((size_t)(t + X.m(i)) * H + h) * D + X.n(j), X.v[i][j]);
         __syncthreads();
         for (int e = threadIdx.x; e < kC * D; e += kThreads)
-            sm.dO[e / D * (D + kPad) + e % D] *= scale * expf((float)sm.b[e / D]);
+            sm.dO[e / D * (D + kPad) + e % D] *= scale * sm.d.row[e / D];
         if (threadIdx.x < 32) {                        // sums from the chunk's end
             const int i = threadIdx.x, r = 31 - i;
             double x = 0.0;
