@@ -1,15 +1,17 @@
 // kda_linear_simt.cuh -- decayed linear attention on CUDA cores, all in fp32:
 // segment states, outputs, and the two halves of the gradient.
 //
-// Serves fp32 inputs (held to 1e-5) at every head size.  32-token
-// chunks: their products and the state update cost the same order of work, and
-// the chunk's tiles and the state fit shared memory at every head size.  Every
-// product is a register tile over operands in shared memory whose rows are
-// padded by one float, so that both row-wise and column-wise reads are free of
-// bank conflicts; shared-memory loads bound it where there are heads enough, and the
-// latency of a chunk's steps where there are few (211 tokens of 3 heads of 64, three
-// chunks at most one after the other: 30 us).  96 heads of 128 x 2,048 tokens: outputs
-// 1.68 ms, gradient 4.38 ms (11 and 10 TFLOP/s of products, of the 71 that these cores have).
+// Serves fp32 inputs (held to 1e-5) at every head size.  32-token chunks: their
+// products and the state update cost the same order of work, and the chunk's tiles and
+// the state fit shared memory at every head size.  Every product is a register tile
+// over operands in shared memory whose rows are padded by four floats, so that reads
+// of 16 bytes along rows and of 4 across them are free of bank conflicts.  Bound by
+// shared-memory reads and FMAs where there are heads enough, by the latency of a
+// chunk's steps where there are few.
+//
+// Measured: 96 heads of 128 x 2,048 tokens, outputs 0.94 ms, gradient 2.11 ms (20 TFLOP/s
+// of products, of the 71 that these cores have; with operands read 4 bytes at a time
+// 1.68 and 4.38 ms); 211 tokens of 3 heads of 64 in 5 sequences 20 us (30 us).
 //
 // Gradient of L = <dO, O> + <dhT, hT>, per chunk with E = dL/dS at its end:
 //   P = Q K^T . D scale,   dP = dO V^T,   dA = dP . D scale
@@ -59,7 +61,9 @@ struct Tile {
         constexpr int kV = kI % 4 == 0 ? 4 : kI % 2 == 0 ? 2 : 1;
         A += TA ? m(0) : m(0) * lda;
         B += TB ? n(0) * ldb : n(0);
-#pragma unroll 2
+        // small tiles have few sums, and need more loads in flight
+        constexpr int kUnroll = kI * kJ <= 4 ? 8 : kI * kJ <= 16 ? 4 : 2;
+#pragma unroll kUnroll
         for (int k = 0; k < K; k += 4) {
             float b[4][kJ];
 #pragma unroll
