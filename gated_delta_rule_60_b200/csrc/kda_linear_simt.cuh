@@ -153,6 +153,7 @@ __device__ __forceinline__ void chunk_decays(Decays &d, const float *g, int per_
 }
 // What the chunk's loads and decays are waited for with.
 __device__ __forceinline__ void chunk_ready() {
+    cp_commit();                                       // a copy in no group is not waited for
     cp_wait_all();
     __syncthreads();
 }
