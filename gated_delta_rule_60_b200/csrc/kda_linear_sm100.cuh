@@ -14,9 +14,14 @@
 // e^{+-60}, far inside the range of bf16 and fp32.  A chunk that decays by more
 // than e^{-120} takes a level for each 32 tokens, all of them powers of two:
 // P'_ij gains the ratio of its row's level to its column's, and the rows of Q are
-// scaled in place by the ratio of theirs to the first (exact).  Where 32 tokens
-// decay by more than e^{-120}, every row takes a level, m = 0 for S'', and P'_ij an
-// exponential of its own.
+// scaled in place by the ratio of theirs to the first (exact).  Levels of
+// neighbouring blocks may be 2^173 apart while the last token of one and the first
+// of the next still see each other, and fp32 ends at 2^-149: what a ratio has below
+// 2^-63 goes to P' behind e^{m - b_j}, so that no step leaves the range before P'
+// itself does (which has decayed by e^{-27} at least then).  A row of Q has a ratio
+// below 2^-126 only where S0 has decayed by e^{-27} too.  Where 32 tokens decay by
+// more than e^{-120}, every row takes a level, m = 0 for S'', and P'_ij an exponential
+// of its own.
 //
 // Precision.  O rounds P' and S'' to bf16 once each (2^-8 of a term); its sum and
 // the row factor are fp32.  S is fp32 in registers and must not take a bf16
@@ -179,6 +184,16 @@ __device__ __noinline__ void direct_block(const Decay &d, uint32_t from, uint32_
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(o[0]),
                      "r"(o[1]), "r"(o[2]), "r"(o[3])
                      : "memory");
+    }
+}
+
+// 32 elements of P' times 2^e
+__device__ __forceinline__ void times_pow2(uint32_t (&o)[16], int e) {
+    const __nv_bfloat162 f = __float2bfloat162_rn(exp2f((float)e));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        __nv_bfloat162 *x = reinterpret_cast<__nv_bfloat162 *>(&o[i]);
+        *x = __hmul2(*x, f);
     }
 }
 
@@ -552,7 +567,8 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                 uint32_t r[32], o[16];
                 tmem_ld32(tq + kColX + 32 * jb, r);
                 const uint32_t whole = jb < w ? 0xffffffffu : 0u;
-                const float ratio = exp2f((float)(level - d.level[jb]));   // 1 on one level
+                const int dl = level - d.level[jb], near = max(dl, -63);   // 0 on one level
+                const float ratio = exp2f((float)near);
                 tmem_wait_ld();
                 if (mode == kFourLevels)
 #pragma unroll
@@ -572,6 +588,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
                     o[j / 2] = pack_bf16(x.x, x.y) & (below[j / 2] | whole);
                     o[j / 2 + 1] = pack_bf16(y.x, y.y) & (below[j / 2 + 1] | whole);
                 }
+                if (dl < near) times_pow2(o, dl - near);
                 tmem_st16(tq + kColP + 16 * jb, o);
             }
             // Q has been read by Q K^T
