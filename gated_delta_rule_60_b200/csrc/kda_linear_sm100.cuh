@@ -99,7 +99,7 @@ struct Small {
     uint64_t full[kStages], dec_free[kStages];
     uint64_t staged[kStages], k_free[kStages];
     uint64_t d1_full, p_ready, o_full, x_free;
-    uint64_t v_full[2], v_free, ds_full, ds_free;
+    uint64_t v_full[2], v_free, ds_full, ds_free, cleared;
     uint64_t drain[2];
     uint32_t tmem;
     volatile int abort;
@@ -212,8 +212,9 @@ __device__ __noinline__ void scale_row(unsigned char *tile, int row, float a) {
 }
 
 // Rows L .. of K and V (the tile behind it) are another sequence's, or nobody's:
-// zero times a NaN there would still be one.  By the 8 warps of S, who read V next
-// and publish S'' (which every product of V waits for) after it.
+// zero times a NaN there would still be one.  By the 8 warps of S, who wait for one
+// another (`cleared`), read V next and publish S'' (which every product of V waits
+// for) after it.
 __device__ __noinline__ void clear_tail(unsigned char *k, int L) {
     const int t = threadIdx.x - 256, row = t >> 1;
     if (row >= L)
@@ -223,7 +224,6 @@ __device__ __noinline__ void clear_tail(unsigned char *k, int L) {
             x[kTile / sizeof(uint4)] = make_uint4(0, 0, 0, 0);
         }
     fence_proxy_async_smem();
-    asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
 struct Params {
@@ -364,6 +364,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         mbar_init(&sm.x_free, 4);
         mbar_init(&sm.ds_full, 1);
         mbar_init(&sm.ds_free, 8);
+        mbar_init(&sm.cleared, 8);
         mbar_init(&sm.drain[0], 1);
         mbar_init(&sm.drain[1], 1);
         sm.abort = 0;
@@ -654,7 +655,11 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             unsigned char *st = sh + slot(c) * Sp::kStage;
             if (hf == 0) {
                 if (!wait(sm, &sm.full[slot(c)], phase(c))) return false;
-                if (len - first(c) < kTok) clear_tail(st + Sp::kK, len - first(c));
+                if (len - first(c) < kTok) {           // one chunk of a segment
+                    clear_tail(st + Sp::kK, len - first(c));
+                    arrive(&sm.cleared);
+                    if (!wait(sm, &sm.cleared, 0)) return false;
+                }
             }
             // the second half's buffer was free once the last chunk's V'^T K was done
             if (hf == 0 && c > 0 && !wait(sm, &sm.v_free, (c - 1) & 1)) return false;
