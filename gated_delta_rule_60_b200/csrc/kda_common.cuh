@@ -26,8 +26,13 @@ __global__ void status_take_kernel(int slot) {
     g_status_taken[slot] = atomicExch(&g_status_word, 0u);
 }
 
-__device__ __forceinline__ void raise_error(unsigned bit) {
+// (on the host, where index arithmetic is tested, there is no word)
+__host__ __device__ __forceinline__ void raise_error(unsigned bit) {
+#ifdef __CUDA_ARCH__
     atomicOr(&g_status_word, bit);
+#else
+    (void)bit;
+#endif
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -74,7 +79,7 @@ struct IO<__nv_bfloat16> {
 
 // Reads the bounds of sequence n.  Returns false (and raises the status bit)
 // when they are malformed; the caller then skips the sequence.
-__device__ __forceinline__ bool seq_bounds(const int32_t *cu, int n, int N,
+__host__ __device__ __forceinline__ bool seq_bounds(const int32_t *cu, int n, int N,
                                            int64_t T_tot, int64_t &start,
                                            int64_t &end) {
     if (cu == nullptr) {

@@ -5,49 +5,7 @@
 namespace kda {
 namespace lin {
 
-
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
-
-// What a plan is made for: how many blocks run at once, and about what a chunk of
-// `tok` tokens costs a block in the main passes and in those that form the segments'
-// states, and what a segment costs the scan (microseconds on a B200; only their ratios
-// and the 8 us of two further launches matter).
-struct Costs {
-    int tok, slots;
-    double main_us, state_us, scan_us;
-};
-
-// Tokens of a segment, for `chains` blocks per sequence.  Equal lengths: the number
-// of segments that minimises the waves of both passes (the first over all segments
-// but the last).  Lengths that the host does not know: a slot's even share of the
-// tokens, which bounds what one long sequence can leave over; sequences below it
-// stay whole.  16 x 131,072 tokens: 9 segments 0.66 ms, 37 0.71 ms, unsplit 3.9 ms; 96 x 8,192:
-// unsplit 0.25 ms, any split adds a pass over all but the last segment.  Half of
-// that share fits one packed batch better and another worse (gradient, 6 documents,
-// 16 heads: 678 -> 640 us; 2 documents, 8 heads: 344 -> 450 us).
-inline int64_t segment_length(int32_t N, bool equal, int64_t T_tot, int64_t chains, const Costs &c) {
-    if (N <= 0 || T_tot <= 0) return kNoSplit;
-    if (!equal && N > 1) {
-        int64_t L = (T_tot * chains + c.slots - 1) / c.slots;
-        if (L < 8 * c.tok) L = 8 * c.tok;
-        L = (L + c.tok - 1) / c.tok * c.tok;
-        return L >= T_tot ? kNoSplit : L;
-    }
-    const int64_t len = (T_tot + N - 1) / N, chunks = (len + c.tok - 1) / c.tok;
-    auto waves = [&](int64_t blocks) { return (double)((blocks + c.slots - 1) / c.slots); };
-    double best = waves(N * chains) * c.main_us * (double)chunks;
-    int64_t L = kNoSplit;
-    for (int64_t G = 2; G <= 64 && G * 4 <= chunks; ++G) {
-        const int64_t per = (chunks + G - 1) / G;
-        const double t = (double)per * (waves(N * chains * G) * c.main_us + waves(N * chains * (G - 1)) * c.state_us) +
-                         8.0 + (double)(N * chains * G) * c.scan_us;
-        if (t < best) {
-            best = t;
-            L = per * c.tok;
-        }
-    }
-    return L;
-}
 
 struct Plan {
     SegMap map;
@@ -68,7 +26,7 @@ inline Plan make_plan(const int32_t *cu, int32_t N, int64_t T_tot, int32_t H, in
     p.map.per = (int)(T_tot / N);
     p.split = L != kNoSplit;
     p.bodies = p.split ? (int)(T_tot / L) : 0;
-    const size_t n = (size_t)p.map.units * H;
+    const size_t n = (size_t)state_slots(T_tot, L, N) * H;
     p.state_bytes = p.split ? align256(n * d * d * sizeof(float)) : 0;
     p.total_bytes = p.split ? align256(n * sizeof(float)) : 0;
     p.factor_bytes = factors ? align256((size_t)(T_tot / mm::kTok + N) * H * sizeof(mm::Factors)) : 0;

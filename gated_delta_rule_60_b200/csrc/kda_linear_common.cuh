@@ -19,6 +19,13 @@
 // meet, the largest is below T_tot / L + N, and a unit finds its sequence by a
 // binary search of cu_seqlens: no table, no launch to build one.  At most N
 // units have no segment and return at once.
+//
+// State slots.  Only a segment of a sequence that is longer than L has a state in
+// the workspace, so segment s of such a sequence has the slot  j + s + min(n, j)
+// with j = start_n / L.  The next such sequence has j' >= j + count - 1 > j and
+// n' > n, so its first slot is behind this one's last; and as j + count - 1 <=
+// T_tot / L, all lie below T_tot / L + min(N, T_tot / L).  (With a state for every
+// unit, the workspace of 4,096 sequences of 96 heads of 128 was 26 GB.)
 #pragma once
 
 #include "kda_common.cuh"
@@ -43,25 +50,32 @@ constexpr int64_t kNoSplit = int64_t(1) << 31;         // segment length of "one
 struct Segment {
     int n;                 // sequence
     int s, count;          // index of the segment, segments of the sequence
+    int slot;              // of its state (count > 1)
     int64_t t0, t1;        // its tokens
 };
 
-__device__ __forceinline__ int64_t seq_begin(const SegMap &m, int n) {
+__host__ __device__ __forceinline__ int64_t seq_begin(const SegMap &m, int n) {
     return m.cu == nullptr ? (int64_t)n * m.per : (int64_t)m.cu[n];
 }
 
-__device__ __forceinline__ int64_t by_length(const SegMap &m, int64_t t) {
+__host__ __device__ __forceinline__ int64_t by_length(const SegMap &m, int64_t t) {
     return (uint32_t)t / (uint32_t)m.L;
 }
 
-__device__ __forceinline__ int64_t unit_base(const SegMap &m, int n) {
+__host__ __device__ __forceinline__ int64_t unit_base(const SegMap &m, int n) {
     return by_length(m, seq_begin(m, n)) + n;
 }
 
+__host__ __device__ inline int64_t state_slots(int64_t T_tot, int64_t L, int64_t N) {
+    const int64_t j = T_tot / L;
+    return j + (N < j ? N : j);
+}
+__host__ __device__ __forceinline__ int state_slot(int n, int j, int s) { return j + s + (n < j ? n : j); }
+
 // The segments of sequence n; false when its bounds are malformed.  With good
 // bounds every unit of the sequence lies in [0, m.units).
-__device__ __forceinline__ bool seq_segments(const SegMap &m, int n, int64_t &start, int64_t &end,
-                                             int &base, int &count) {
+__host__ __device__ __forceinline__ bool seq_segments(const SegMap &m, int n, int64_t &start, int64_t &end,
+                                                      int &base, int &count) {
     start = seq_begin(m, n);
     end = start + m.per;
     if (m.cu != nullptr && !seq_bounds(m.cu, n, m.N, m.T_tot, start, end)) return false;
@@ -71,7 +85,7 @@ __device__ __forceinline__ bool seq_segments(const SegMap &m, int n, int64_t &st
 }
 
 // The segment of unit u; false when it has none.
-__device__ __forceinline__ bool find_segment(const SegMap &m, int u, Segment &g) {
+__host__ __device__ __forceinline__ bool find_segment(const SegMap &m, int u, Segment &g) {
     int lo = 0, hi = m.N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -84,6 +98,7 @@ __device__ __forceinline__ bool find_segment(const SegMap &m, int u, Segment &g)
     if (!seq_segments(m, lo, start, end, base, g.count)) return false;
     g.s = u - base;
     if (g.s < 0 || g.s >= g.count) return false;
+    g.slot = state_slot(lo, base - lo, g.s);
     g.t0 = start + (int64_t)g.s * m.L;
     g.t1 = g.t0 + m.L < end ? g.t0 + m.L : end;
     return true;
@@ -120,8 +135,8 @@ __device__ __forceinline__ int ranked_unit(const SegMap &m, int rank, int *len) 
 // or in reverse the first), are numbered without gaps for short sequences:
 // segment i of them has the number start_n / L + i.  A sequence with any is longer
 // than L, so the numbers never meet, all lie below T_tot / L, and the owner of a
-// number is the last sequence that starts at or below it.  u: its unit.
-__device__ __forceinline__ bool find_body(const SegMap &m, int64_t j, bool reverse, Segment &g, int &u) {
+// number is the last sequence that starts at or below it.
+__host__ __device__ __forceinline__ bool find_body(const SegMap &m, int64_t j, bool reverse, Segment &g) {
     int lo = 0, hi = m.N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -135,10 +150,51 @@ __device__ __forceinline__ bool find_body(const SegMap &m, int64_t j, bool rever
     const int64_t i = j - by_length(m, start);
     if (i < 0 || i >= g.count - 1) return false;
     g.s = (int)i + (reverse ? 1 : 0);
-    u = base + g.s;
+    g.slot = state_slot(lo, base - lo, g.s);
     g.t0 = start + (int64_t)g.s * m.L;
     g.t1 = g.t0 + m.L < end ? g.t0 + m.L : end;
     return true;
+}
+
+// What a plan is made for: how many blocks run at once, and about what a chunk of
+// `tok` tokens costs a block in the main passes and in those that form the segments'
+// states, and what a segment costs the scan (microseconds on a B200; only their ratios
+// and the 8 us of two further launches matter).
+struct Costs {
+    int tok, slots;
+    double main_us, state_us, scan_us;
+};
+
+// Tokens of a segment, for `chains` blocks per sequence.  Equal lengths: the number
+// of segments that minimises the waves of both passes (the first over all segments
+// but the last).  Lengths that the host does not know: a slot's even share of the
+// tokens, which bounds what one long sequence can leave over; sequences below it
+// stay whole.  16 x 131,072 tokens: 9 segments 0.66 ms, 37 0.71 ms, unsplit 3.9 ms; 96 x 8,192:
+// unsplit 0.25 ms, any split adds a pass over all but the last segment.  Half of
+// that share fits one packed batch better and another worse (gradient, 6 documents,
+// 16 heads: 678 -> 640 us; 2 documents, 8 heads: 344 -> 450 us).
+inline int64_t segment_length(int32_t N, bool equal, int64_t T_tot, int64_t chains, const Costs &c) {
+    if (N <= 0 || T_tot <= 0) return kNoSplit;
+    if (!equal && N > 1) {
+        int64_t L = (T_tot * chains + c.slots - 1) / c.slots;
+        if (L < 8 * c.tok) L = 8 * c.tok;
+        L = (L + c.tok - 1) / c.tok * c.tok;
+        return L >= T_tot ? kNoSplit : L;
+    }
+    const int64_t len = (T_tot + N - 1) / N, chunks = (len + c.tok - 1) / c.tok;
+    auto waves = [&](int64_t blocks) { return (double)((blocks + c.slots - 1) / c.slots); };
+    double best = waves(N * chains) * c.main_us * (double)chunks;
+    int64_t L = kNoSplit;
+    for (int64_t G = 2; G <= 64 && G * 4 <= chunks; ++G) {
+        const int64_t per = (chunks + G - 1) / G;
+        const double t = (double)per * (waves(N * chains * G) * c.main_us + waves(N * chains * (G - 1)) * c.state_us) +
+                         8.0 + (double)(N * chains * G) * c.scan_us;
+        if (t < best) {
+            best = t;
+            L = per * c.tok;
+        }
+    }
+    return L;
 }
 
 // The whole of cu_seqlens is checked by one block (every other access relies on
@@ -228,7 +284,7 @@ __device__ __forceinline__ void split3(float2 x, uint32_t &hi, uint32_t &mid, ui
     lo = pack_cut(x);
 }
 
-// Scan over the segments of one (sequence, head): on entry ws[u][h] holds the
+// Scan over the segments of one (sequence, head): on entry ws[slot][h] holds the
 // segment's R, on return the state it starts from (forward) or the gradient of
 // the state it ends in (reverse).  Elementwise, so bound by memory: one read and
 // one write of each R.  grid (elements / 1024, H, scan_blocks): equal sequences one
@@ -253,14 +309,15 @@ segment_scan_kernel(SegMap m, int H, int dd, const float *init, const float *__r
     const int64_t blocks = scan_blocks(m);
     for (int64_t j = blockIdx.z; j < blocks; j += gridDim.z) {
         Segment g;
-        int base;
         if (m.cu != nullptr) {
-            if (!find_body(m, j, false, g, base) || g.s != 0) continue;
+            if (!find_body(m, j, false, g) || g.s != 0) continue;
         } else {
+            int base;
             g.n = (int)j;
             if (!seq_segments(m, g.n, g.t0, g.t1, base, g.count)) continue;
+            g.slot = state_slot(g.n, base - g.n, 0);
         }
-        const int first = kReverse ? base + g.count - 1 : base;
+        const int first = kReverse ? g.slot + g.count - 1 : g.slot;
         float *p = ws + ((size_t)first * H + h) * dd + e;
         const float *t = total + (size_t)first * H + h;
         float4 S = make_float4(0.f, 0.f, 0.f, 0.f);

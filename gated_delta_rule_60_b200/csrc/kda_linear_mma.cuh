@@ -377,9 +377,8 @@ state_kernel(const bf16 *__restrict__ x, const bf16 *__restrict__ y, const Facto
     extern __shared__ __align__(16) unsigned char raw[];
     StateSmem<D> &sm = *reinterpret_cast<StateSmem<D> *>(raw);
     const int h = blockIdx.x % H;
-    int u;
     Segment sg;
-    if (!find_body(m, blockIdx.x / H, kReverse, sg, u)) return;
+    if (!find_body(m, blockIdx.x / H, kReverse, sg)) return;
     const Walk w = make_walk(sg, kReverse);
     const int hk = h / (H / Hk);
     const int64_t slot = first_slot(m, sg);
@@ -402,8 +401,8 @@ state_kernel(const bf16 *__restrict__ x, const bf16 *__restrict__ y, const Facto
                         f.gamma);
         sum = add2(sum, {f.end_hi, f.end_lo});
     }
-    store_state<D, false>(X, ws + ((size_t)u * H + h) * D * D);
-    if (threadIdx.x == 0) total[(size_t)u * H + h] = exp_sum(sum);
+    store_state<D, false>(X, ws + ((size_t)sg.slot * H + h) * D * D);
+    if (threadIdx.x == 0) total[(size_t)sg.slot * H + h] = exp_sum(sum);
 }
 
 // -------------------------------------------------------------- outputs
@@ -431,7 +430,7 @@ out_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16 *_
     const Walk w = make_walk(sg, false);
     const int hk = h / (H / Hk), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int64_t slot = first_slot(m, sg);
-    const float *from = ws != nullptr && sg.count > 1 ? ws + ((size_t)u * H + h) * D * D
+    const float *from = ws != nullptr && sg.count > 1 ? ws + ((size_t)sg.slot * H + h) * D * D
                         : h0 != nullptr ? h0 + ((size_t)sg.n * H + h) * D * D : nullptr;
     float X[D / 8][4];
     load_state<D, true>(X, from);
@@ -646,7 +645,7 @@ grad_q_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf16
     const Walk w = make_walk(sg, false);
     const int hk = h / (H / Hk), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int64_t slot = first_slot(m, sg);
-    const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
+    const size_t seg = ((size_t)sg.slot * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
     float X[D / 8][4];
     load_state<D, false>(X, wsS != nullptr && sg.count > 1 ? wsS + seg : h0 != nullptr ? h0 + seq : nullptr);
     auto load = [&](int i) {
@@ -736,7 +735,7 @@ grad_kv_kernel(const bf16 *__restrict__ q, const bf16 *__restrict__ k, const bf1
     const Walk w = make_walk(sg, true);
     const int hk = h / (H / Hk), warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int64_t slot = first_slot(m, sg);
-    const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
+    const size_t seg = ((size_t)sg.slot * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
     float X[D / 8][4];
     load_state<D, false>(X, wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr);
     auto load = [&](int i) {

@@ -179,9 +179,8 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
     extern __shared__ __align__(16) unsigned char raw[];
     Sm &sm = *reinterpret_cast<Sm *>(raw);
     const int h = blockIdx.y, c0 = blockIdx.z * W;
-    int u;
     Segment sg;
-    if (!find_body(m, blockIdx.x, kReverse, sg, u)) return;
+    if (!find_body(m, blockIdx.x, kReverse, sg)) return;
     Tile<D, W> S;
     S.zero();
     double sum = 0.0;
@@ -210,12 +209,12 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
         __syncthreads();
         S.template mac<kC, true, false>(sm.x, D + kPad, sm.y, W + kPad);
     }
-    float *out = ws + ((size_t)u * H + h) * D * D + c0;
+    float *out = ws + ((size_t)sg.slot * H + h) * D * D + c0;
 #pragma unroll
     for (int i = 0; i < S.kI; ++i)
 #pragma unroll
         for (int j = 0; j < S.kJ; ++j) out[(size_t)S.m(i) * D + S.n(j)] = S.v[i][j];
-    if (c0 == 0 && threadIdx.x == 0) total[(size_t)u * H + h] = expf((float)sum);
+    if (c0 == 0 && threadIdx.x == 0) total[(size_t)sg.slot * H + h] = expf((float)sum);
 }
 
 // -------------------------------------------------------------- outputs
@@ -242,7 +241,7 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
     if (u == 0 && h == 0 && c0 == 0) check_seqlens(m);
     Segment sg;
     if (!find_segment(m, u, sg)) return;
-    const float *from = ws != nullptr && sg.count > 1 ? ws + ((size_t)u * H + h) * D * D
+    const float *from = ws != nullptr && sg.count > 1 ? ws + ((size_t)sg.slot * H + h) * D * D
                         : h0 != nullptr ? h0 + ((size_t)sg.n * H + h) * D * D : nullptr;
     Tile<D, W> S;
 #pragma unroll
@@ -376,7 +375,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     if (u == 0 && h == 0) check_seqlens(m);
     Segment sg;
     if (!find_segment(m, u, sg)) return;
-    const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
+    const size_t seg = ((size_t)sg.slot * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
     const float *from = wsS != nullptr && sg.count > 1 ? wsS + seg : h0 != nullptr ? h0 + seq : nullptr;
     Tile<D, D> S;
 #pragma unroll
@@ -474,7 +473,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
         if (!per_token && threadIdx.x == 0) head_sum[(size_t)u * H + h] = 0.0;
         return;
     }
-    const size_t seg = ((size_t)u * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
+    const size_t seg = ((size_t)sg.slot * H + h) * D * D, seq = ((size_t)sg.n * H + h) * D * D;
     const float *from = wsE != nullptr && sg.count > 1 ? wsE + seg : dhT != nullptr ? dhT + seq : nullptr;
     Tile<D, D> E;
 #pragma unroll

@@ -336,14 +336,13 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
     auto phase = [](int c) { return kStages == 2 ? (c >> 1) & 1 : (c / kStages) & 1; };
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int h = blockIdx.x % p.H;
-    int u = blockIdx.x / p.H;
+    const int i = blockIdx.x / p.H;
     if (!kStates && blockIdx.x == 0) check_seqlens(p.m);
     Segment sg;
     if (kStates) {                                     // all of one length, but for sequence ends
-        if (!find_body(p.m, u, kReverse, sg, u)) return;
+        if (!find_body(p.m, i, kReverse, sg)) return;
     } else {
-        u = ranked_unit<kThreads>(p.m, u, reinterpret_cast<int *>(sh));
-        if (!find_segment(p.m, u, sg)) return;
+        if (!find_segment(p.m, ranked_unit<kThreads>(p.m, i, reinterpret_cast<int *>(sh)), sg)) return;
     }
     const int len = (int)(sg.t1 - sg.t0);
     const int chunks = (len + kTok - 1) / kTok;
@@ -506,7 +505,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             store_decay(sm.dec[slot(c)], d);
             arrive(&sm.full[slot(c)]);
         }
-        if (kStates && lane == 0) p.total[(size_t)u * p.H + h] = exp_sum(sum);
+        if (kStates && lane == 0) p.total[(size_t)sg.slot * p.H + h] = exp_sum(sum);
     } else if (warp == 3) {
         // ------------------------------------------------------------ V'^T K
         constexpr uint32_t id = idesc_bf16(128, 128, false, true);
@@ -643,7 +642,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
         float S[64];
         const float *from = nullptr;
         if (!kStates) {
-            if (p.ws != nullptr && sg.count > 1) from = p.ws + ((size_t)u * p.H + h) * kD * kD;
+            if (p.ws != nullptr && sg.count > 1) from = p.ws + ((size_t)sg.slot * p.H + h) * kD * kD;
             else if (p.h0 != nullptr) from = p.h0 + ((size_t)sg.n * p.H + h) * kD * kD;
         }
 #pragma unroll
@@ -765,7 +764,7 @@ linear_sm100_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_cons
             if (!kStates && ok && c + 1 < chunks) publish(c + 1);
         }
         float *to = nullptr;
-        if (kStates) to = p.out + ((size_t)u * p.H + h) * kD * kD;
+        if (kStates) to = p.out + ((size_t)sg.slot * p.H + h) * kD * kD;
         else if (p.out != nullptr && sg.s == sg.count - 1) to = p.out + ((size_t)sg.n * p.H + h) * kD * kD;
         if (ok && to != nullptr)
 #pragma unroll
