@@ -85,16 +85,23 @@ inline BwdSizes bwd_sizes(const Plan &p, int64_t T_tot, int32_t Hk, int32_t H, i
 
 inline bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 
-// Checks that the prefill and its gradient share; KDA_OK leaves `empty` true
-// when there is nothing to do.
-inline kda_status check_shapes(int32_t N, int64_t T_tot, int32_t Hk, int32_t H, int32_t d,
-                               kda_dtype dt, const int32_t *cu, float scale, bool &empty) {
-    empty = false;
+// Sizes that the prefill and its gradient take.
+inline kda_status check_sizes(int32_t N, int64_t T_tot, int32_t Hk, int32_t H, int32_t d, kda_dtype dt) {
     if (N < 0 || T_tot < 0 || H <= 0 || Hk <= 0 || H > 65535 || H % Hk != 0)
         return KDA_ERR_INVALID_ARGUMENT;
     if (dt != KDA_BF16 && dt != KDA_FP32) return KDA_ERR_UNSUPPORTED;
     if (!supported_d(d)) return KDA_ERR_UNSUPPORTED;
     if (T_tot > kMaxTokensSm100) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)N * H > 0x7fffffff || T_tot / 64 + N > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
+    return KDA_OK;
+}
+
+// The rest of their checks; KDA_OK leaves `empty` true when there is nothing to do.
+inline kda_status check_shapes(int32_t N, int64_t T_tot, int32_t Hk, int32_t H, int32_t d,
+                               kda_dtype dt, const int32_t *cu, float scale, bool &empty) {
+    empty = false;
+    const kda_status st = check_sizes(N, T_tot, Hk, H, d, dt);
+    if (st != KDA_OK) return st;
     if (!(scale - scale == 0.f)) return KDA_ERR_INVALID_ARGUMENT;       // inf or NaN
     if (N == 0) {
         empty = true;
@@ -102,7 +109,6 @@ inline kda_status check_shapes(int32_t N, int64_t T_tot, int32_t Hk, int32_t H, 
     }
     if (cu == nullptr && (T_tot % N) != 0) return KDA_ERR_INVALID_ARGUMENT;
     if (cu != nullptr && !aligned16(cu)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((int64_t)N * H > 0x7fffffff || T_tot / 64 + N > 0x7fffffff) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
 }
 
@@ -453,8 +459,7 @@ kda_status step_any(kda_dtype dt, const void *q, const void *k, const void *v, c
 extern "C" KDA_API size_t kda_linear_chunk_fwd_workspace_size(int32_t N, int64_t T_tot, int32_t H,
                                                               int32_t d, kda_dtype dt) {
     using namespace kda::lin;
-    if (N <= 0 || T_tot < 0 || H <= 0 || !supported_d(d)) return 0;
-    if (dt != KDA_BF16 && dt != KDA_FP32) return 0;
+    if (N <= 0 || check_sizes(N, T_tot, 1, H, d, dt) != KDA_OK) return 0;
     const size_t a = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, false, T_tot, H, d, dt), fwd_factors(d, dt)));
     const size_t b = fwd_bytes(make_plan(nullptr, N, T_tot, H, d, fwd_length(N, true, T_tot, H, d, dt), fwd_factors(d, dt)));
     return a > b ? a : b;
@@ -507,8 +512,7 @@ extern "C" KDA_API size_t kda_linear_chunk_bwd_workspace_size(int32_t N, int64_t
                                                               int32_t Hk, int32_t H, int32_t d,
                                                               kda_dtype dt) {
     using namespace kda::lin;
-    if (N <= 0 || T_tot < 0 || H <= 0 || Hk <= 0 || !supported_d(d)) return 0;
-    if (dt != KDA_BF16 && dt != KDA_FP32) return 0;
+    if (N <= 0 || check_sizes(N, T_tot, Hk, H, d, dt) != KDA_OK) return 0;
     size_t most = 0;
     for (int equal = 0; equal < 2; ++equal) {
         const Plan p = make_plan(nullptr, N, T_tot, H, d, bwd_length(N, equal, T_tot, H, d, dt), dt == KDA_BF16);

@@ -270,7 +270,8 @@ KDA_API kda_status kda_prologue(const void *xq, const void *xk, const void *xv,
  *   cu_seqlens, N, T_tot                   as for kda_chunk_fwd
  *   scale       finite
  *   workspace   kda_linear_chunk_fwd_workspace_size() bytes, 256-byte aligned
- *               (NULL when that is 0): the states between segments
+ *               (NULL when that is 0, as it also is for sizes that are refused):
+ *               the states between segments
  *
  * dt KDA_BF16 or KDA_FP32, d in {16, 32, 64, 128}, H <= 65535, N * H below
  * 2^31.  The decay sums are formed in fp64, states and every product's sum in
