@@ -8,10 +8,11 @@
 // also the gradient.
 //
 // Angles of far positions: fp32 loses pos * f to 0.06 rad at a million tokens, so
-// the product is formed in fp64, turned into revolutions, reduced to [-1/2, 1/2]
-// there, and only then given to sincospi in fp32 (2e-7 rad).  A block computes the
-// rot / 2 angles of its tokens once, into shared memory, for all of its heads:
-// with H heads that is one angle per 2 H values.
+// the product is formed in revolutions in fp64, with what its roundings leave (at
+// 2^31 alone they are off by 5e-7 rad), reduced to [-1/2, 1/2] there, and only then
+// given to sincospi in fp32 (2e-7 rad).  A block computes the rot / 2 angles of its
+// tokens once, into shared memory, for all of its heads: with H heads that is one
+// angle per 2 H values.
 //
 // Measured: q and k of 8,192 tokens, 96 heads of 128 139 us (5.8 TB/s); a step of 256
 // tokens, 96 and 8 heads, half of 128 channels turned 5.3 us, most of it the fp64
@@ -108,6 +109,16 @@ __device__ __forceinline__ int64_t position(const Args &a, int64_t t) {
     return t - a.cu[lo];
 }
 
+// pos * f / 2 pi less its nearest whole number: 1 / 2 pi and both products as sums of
+// two doubles.
+__device__ __forceinline__ double turns(int64_t pos, float f) {
+    constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+    const double x = f, p = (double)pos;
+    const double hi = x * kHi, lo = fma(x, kHi, -hi) + x * kLo;
+    const double t = p * hi;
+    return (t - rint(t)) + (fma(p, hi, -t) + p * lo);
+}
+
 // grid (token tiles, head slices).  V = 1 or a full 16-byte vector; kPairs:
 // neighbours are paired.  One work item of a head is V pairs: for halves the
 // vectors at i and i + rot / 2, for neighbours the 2 V values at 2 i (two
@@ -126,10 +137,8 @@ rotary_kernel(const T *q, const T *k, const float *__restrict__ freq, Args a, T 
         if (!ok) raise_error(kErrSeqlens);
     }
     for (int e = threadIdx.x; e < nt * half; e += kThreads) {
-        const double turns =
-            (double)position(a, t0 + e / half) * ((double)freq[e % half] * 0.15915494309189533577);
         float s, c;
-        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+        sincospif((float)(2.0 * turns(position(a, t0 + e / half), freq[e % half])), &s, &c);
         cs[e] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
     }
     __syncthreads();
