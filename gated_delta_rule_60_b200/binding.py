@@ -14,7 +14,7 @@ a torch.cuda.device context); stream=None means that device's current stream.
 import ctypes
 import functools
 import os
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
@@ -863,20 +863,27 @@ def kda_layernorm_bwd_workspace_size(T: int, G: int, D: int, dtype: torch.dtype)
 
 
 def kda_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
-                      weight: Optional[torch.Tensor] = None, *, bias: bool = False,
+                      weight: Optional[torch.Tensor] = None, *,
+                      bias: Union[bool, torch.Tensor, None] = False,
                       dx: Optional[torch.Tensor] = None,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Gradient of kda_layernorm_fwd: a dict of dx (dtype of x), dweight (with
-    a weight) and dbias (with bias=True), fp32 of the weight's shape (a bias
-    without a weight: [D])."""
+    a weight) and dbias (with a bias), fp32 of the weight's shape.  bias: the
+    forward's, whose shape alone counts, or True for one of the weight's shape
+    (without a weight: [D])."""
     lib = load_library()
-    idx, T, G, D, dt, code = _norm_sizes(x, weight)
+    given = isinstance(bias, torch.Tensor)
+    idx, T, G, D, dt, code = _norm_sizes(x, weight if weight is not None or not given else bias)
     shape = x.shape
     px, pdy = _at(x, "x", dt, shape, idx), _at(dy, "dy", dt, shape, idx)
     pm = _at(mean, "mean", torch.float32, shape[:-1], idx)
     pr = _at(rstd, "rstd", torch.float32, shape[:-1], idx)
-    of = (G, D) if weight is not None and weight.dim() == 2 else (D,)
+    by = weight if weight is not None else bias if given else None
+    of = (G, D) if by is not None and by.dim() == 2 else (D,)
     pw = _maybe(weight, "weight", torch.float32, of, idx)
+    if given:
+        _at(bias, "bias", torch.float32, of, idx)
+    bias = given or bool(bias)
     handle = _stream_at(stream, idx)
     if dx is None:
         dx = _empty(stream, idx, shape, dt)
