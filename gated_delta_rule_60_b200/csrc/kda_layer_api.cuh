@@ -52,9 +52,11 @@ namespace ln {
 constexpr int kMaxD = 8192;
 
 // The smallest row share that holds D values, and the values of a thread: 16 up to
-// 512, then 64 bytes of them.
+// 512, then 64 bytes of them.  The widest rows take 256 threads in bf16, 512 in fp32.
 template <typename T>
 constexpr int long_per() { return 64 / (int)sizeof(T); }
+template <typename T>
+constexpr int widest() { return kMaxD / long_per<T>(); }
 #define KDA_LN_DISPATCH(T, D, CALL)                         \
     ((D) <= 32                   ? CALL(2, 16)              \
      : (D) <= 128                ? CALL(8, 16)              \
@@ -62,7 +64,7 @@ constexpr int long_per() { return 64 / (int)sizeof(T); }
      : (D) <= 64 * long_per<T>() ? CALL(64, long_per<T>())  \
      : (D) <= 128 * long_per<T>() ? CALL(128, long_per<T>()) \
      : (D) <= 256 * long_per<T>() ? CALL(256, long_per<T>()) \
-                                  : CALL(512, 16))
+                                  : CALL(widest<T>(), long_per<T>()))
 
 // Threads that share a row.
 inline int row_share(int D, kda_dtype dt) {
@@ -90,12 +92,18 @@ inline Grid make_grid(int64_t tokens, int G, int tpr, int per_sm) {
 // rows on their way.
 constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
 
+// A row can fill its share only where D is a multiple of a full vector.
+template <typename T, int V>
+constexpr bool may_fill() { return V * sizeof(T) == 16; }
+
 template <typename T, int V, int kTpr, int kPer>
 kda_status fwd_at(const void *x, const float *w, const float *b, int64_t tokens, int G, int D,
                   float eps, void *y, float *mean, float *rstd, cudaStream_t s) {
     constexpr int kNV = kPer / V, kThreads = Block<kTpr>::kThreads;
     const Grid g = make_grid(tokens, G, kTpr, kFwdPerSm);
-    auto kern = D == kTpr * V * kNV ? fwd_kernel<T, V, kTpr, kNV, true> : fwd_kernel<T, V, kTpr, kNV, false>;
+    auto kern = fwd_kernel<T, V, kTpr, kNV, false>;
+    if constexpr (may_fill<T, V>())
+        if (D == kTpr * V * kNV) kern = fwd_kernel<T, V, kTpr, kNV, true>;
     const size_t smem = Feed<T, V, kNV, kThreads, 1>::kSmem;
     if (!lin::set_smem(kern, smem)) return KDA_ERR_CUDA;
     kern<<<dim3((unsigned)g.blocks, (unsigned)(G / g.gs)), kThreads, smem, s>>>(
@@ -119,8 +127,9 @@ kda_status bwd_at(const void *dy, const void *x, const float *mean, const float 
     const Grid g = make_grid(tokens, G, kTpr, kBwdPerSm);
     const size_t sums = kRows != g.gs && part ? (size_t)kRows * D * sizeof(float) : 0;
     const size_t rows = Feed<T, V, kNV, kThreads, 2>::kSmem, smem = std::max(rows, sums);
-    auto kern = D == kTpr * V * kNV ? bwd_kernel<T, V, kTpr, kNV, true, kBias>
-                                    : bwd_kernel<T, V, kTpr, kNV, false, kBias>;
+    auto kern = bwd_kernel<T, V, kTpr, kNV, false, kBias>;
+    if constexpr (may_fill<T, V>())
+        if (D == kTpr * V * kNV) kern = bwd_kernel<T, V, kTpr, kNV, true, kBias>;
     if (!lin::set_smem(kern, smem)) return KDA_ERR_CUDA;
     kern<<<dim3((unsigned)g.blocks, (unsigned)(G / g.gs)), kThreads, smem, s>>>(
         (const T *)dy, (const T *)x, mean, rstd, w, tokens, G, g.gs, D, (T *)dx, part);
