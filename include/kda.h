@@ -274,10 +274,12 @@ KDA_API kda_status kda_prologue(const void *xq, const void *xk, const void *xv,
  *               the states between segments
  *
  * dt KDA_BF16 or KDA_FP32, d in {16, 32, 64, 128}, H <= 65535, N * H below
- * 2^31.  The decay sums are formed in fp64, states and every product's sum in
- * fp32.  q, k, v are finite: a NaN or an infinity at one token may reach the
- * outputs of the tokens of its 128-token chunk that come before it.  Status as
- * for kda_chunk_fwd.
+ * 2^31.  The decay sums are formed in 48 bits (bf16: pairs of floats) or fp64,
+ * states and every product's sum in fp32.  q, k, v are finite: a NaN or an
+ * infinity at one token may reach the outputs of the tokens of its 128-token
+ * chunk that come before it.  In bf16 at d = 128, where decay factors up to e^60
+ * are formed, |q.k| |v| and the states are also to stay below 1e11, and what is
+ * below 1e-11 in an output may lose bits.  Status as for kda_chunk_fwd.
  */
 KDA_API size_t kda_linear_chunk_fwd_workspace_size(int32_t N, int64_t T_tot, int32_t H, int32_t d,
                                                    kda_dtype dt);

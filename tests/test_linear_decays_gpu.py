@@ -10,8 +10,9 @@ import pytest
 import torch
 
 from gated_delta_rule_60_b200 import binding
-from linear_testutil import make
-from test_linear_gpu import _check_bwd, _check_fwd
+from linear_testutil import BF16, SUM, close, make, sizes
+from oracle import linear_ops as lo
+from test_linear_gpu import _check_bwd, _check_fwd, _fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +134,24 @@ def test_constant_decays_across_segments():
     assert min(forms.values()) > 8, forms
     _check_fwd(x, cu)
     _check_bwd(x, cu, plain_decay=False)
+
+
+@pytest.mark.parametrize("size", [1e-11, 1e11])
+def test_the_range_of_the_values(size):
+    """Values and states of the smallest and largest size that the forms are promised
+    for.  The state that queries read is rounded to bf16 behind a factor of e^{-60} at
+    least, and bf16 ends in steps of 2^-133: half of one is 2^-134 e^{60} = 5.2e-15 of
+    an output for every unit of |q|, of which a query has sqrt(128) at most: 5.9e-14.
+    Products end in steps of 2^-149 in fp32: 256 of 1.6e-19 are 4e-17 besides."""
+    decays = (-0.3, -0.9, -0.93, -3.0, -3.7, -5.0)
+    x, cu = _make([300], len(decays), h0=True, seed=206)
+    x["g"] = torch.tensor(decays)
+    x["v"] = (x["v"].float() * size).to(BF)
+    x["h0"] = x["h0"] * size
+    o, hT = _fwd(x, cu)
+    ro, rh = lo.linear_forward(x["q"], x["k"], x["v"], x["g"], cu, x["h0"])
+    a = sizes(x)
+    so, sh = lo.linear_forward(a["q"], a["k"], a["v"], a["g"], cu, a["h0"])
+    got = o.double().cpu().numpy()
+    assert np.all(np.abs(got - ro) <= SUM * so + BF16 * (np.abs(ro) + so) + 6e-14)
+    close(hT, rh, sh, torch.float32, "hT")
