@@ -224,6 +224,8 @@ extern "C" KDA_API kda_status kda_rotary(const void *q, const void *k, const flo
     // in place only over the whole layout
     if ((q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
         return KDA_ERR_INVALID_ARGUMENT;
+    // an output that starts where the other one, or the other input, does
+    if (Hk > 0 && (q_out == k_out || q_out == k || k_out == q)) return KDA_ERR_INVALID_ARGUMENT;
     kda::rotary::Args a;
     a.pos = positions;
     a.cu = cu_seqlens;

@@ -336,7 +336,9 @@ KDA_API kda_status kda_linear_chunk_bwd(const void *q, const void *k, const void
  *   q, q_out    device, Hq heads of d (dt) at stride q_stride / q_out_stride
  *               elements between tokens (at least Hq * d); q_out may be q with
  *               the same stride (in place), and may not overlap it otherwise
- *   k, k_out    the same with Hk heads; Hk = 0 leaves k out
+ *   k, k_out    the same with Hk heads; Hk = 0 leaves k out.  q_out overlaps
+ *               neither k nor k_out, and k_out not q (rows of one array beside
+ *               one another do not overlap)
  *   inv_freq    device fp32 [rot / 2]
  *   positions   device int32 [T_tot], or NULL: the index of the token in its
  *               sequence by cu_seqlens / N (as for kda_chunk_fwd)
