@@ -165,7 +165,7 @@ kda_status fwd_simt(const Plan &p, const FwdArgs &a, cudaStream_t s) {
     if (p.split) {
         states = reinterpret_cast<float *>(a.ws);
         total = reinterpret_cast<float *>(a.ws + p.state_bytes);
-        auto kern = state_kernel<float, D, false>;
+        auto kern = state_kernel<D, false>;
         const size_t smem = sizeof(StateSmem<D>);
         const dim3 bodies((unsigned)p.bodies, grid.y, grid.z);
         if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
@@ -174,7 +174,7 @@ kda_status fwd_simt(const Plan &p, const FwdArgs &a, cudaStream_t s) {
         if (st == KDA_OK) st = launch_scan<false>(p, a.H, D, a.h0, total, states, s);
         if (st != KDA_OK) return st;
     }
-    auto kern = out_kernel<float, D>;
+    auto kern = out_kernel<D>;
     const size_t smem = sizeof(OutSmem<D>);
     if (!set_smem(kern, smem)) return KDA_ERR_CUDA;
     kern<<<grid, kThreads, smem, s>>>(q, k, v, a.g, a.per_token, a.h0, p.map, a.Hk, a.H, a.scale, states,
@@ -329,8 +329,8 @@ kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
     if (p.split) {
         const dim3 grid((unsigned)p.bodies, (unsigned)a.H, (unsigned)(D / StateSmem<D>::kW));
         const size_t smem = sizeof(StateSmem<D>);
-        auto fs = state_kernel<float, D, false>;
-        auto rs = state_kernel<float, D, true>;
+        auto fs = state_kernel<D, false>;
+        auto rs = state_kernel<D, true>;
         if (!set_smem(fs, smem) || !set_smem(rs, smem)) return KDA_ERR_CUDA;
         fs<<<grid, kThreads, smem, s>>>(k, v, a.g, a.per_token, p.map, a.Hk, a.H, 1.f, b.S, b.totS);
         rs<<<grid, kThreads, smem, s>>>(q, dO, a.g, a.per_token, p.map, a.Hk, a.H, a.scale, b.E, b.totE);
@@ -341,8 +341,8 @@ kda_status bwd_simt(const Plan &p, const BwdArgs &a, cudaStream_t s) {
     }
     const dim3 grid((unsigned)p.map.units, (unsigned)a.H);
     const size_t smem = sizeof(GradSmem<D>);
-    auto kq = grad_q_kernel<float, D>;
-    auto kkv = grad_kv_kernel<float, D>;
+    auto kq = grad_q_kernel<D>;
+    auto kkv = grad_kv_kernel<D>;
     if (!set_smem(kq, smem) || !set_smem(kkv, smem)) return KDA_ERR_CUDA;
     kq<<<grid, kThreads, smem, s>>>(q, k, v, dO, a.g, a.per_token, a.h0, a.dhT, p.map, a.Hk, a.H, a.scale, b.S, b.E,
                                     (float *)a.dq, b.part, b.term, b.anchor);

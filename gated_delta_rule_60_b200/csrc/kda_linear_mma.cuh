@@ -535,7 +535,7 @@ __device__ __forceinline__ void inside_chunk(GradSmem<D> &sm, int buf, const Fac
         const int r0 = 16 * (x >> 1), n0 = 32 * (x & 1);
         if (n0 > r0 + 15) {                            // above the diagonal: sums of nothing
             if (kRows && (lane & 3) == 0) sm.inner[x & 1][r0 + (lane >> 2)] = sm.inner[x & 1][r0 + 8 + (lane >> 2)] = 0.f;
-            if (!kRows && lane < 32) sm.inner[x >> 1][n0 + lane] = 0.f;
+            if (!kRows) sm.inner[x >> 1][n0 + lane] = 0.f;
             continue;
         }
         float c[4][4], d[4][4];

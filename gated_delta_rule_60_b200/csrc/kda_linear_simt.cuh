@@ -122,10 +122,9 @@ __device__ __forceinline__ float row_sum(float x) {
 
 // [kC][W] tile of rows t0 .. t0 + len of x [T, heads, D], columns c0 .. c0 + W,
 // zero behind len (a row of zeros with log-decay 0 leaves every result alone).
-template <typename T, int W>
-__device__ __forceinline__ void load_tile(float *dst, const T *x, int64_t t0, int len, int heads,
+template <int W>
+__device__ __forceinline__ void load_tile(float *dst, const float *x, int64_t t0, int len, int heads,
                                           int head, int D, int c0) {
-    static_assert(sizeof(T) == sizeof(float), "copied as fp32");
     for (int e = threadIdx.x; e < kC * W / 4; e += kThreads) {
         const int r = e / (W / 4), c = e % (W / 4) * 4;
         const size_t row = t0 + (r < len ? r : 0);
@@ -169,9 +168,9 @@ struct StateSmem {
     Decays d;
 };
 
-template <typename T, int D, bool kReverse>
+template <int D, bool kReverse>
 __global__ void __launch_bounds__(kThreads)
-state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__restrict__ g,
+state_kernel(const float *__restrict__ x, const float *__restrict__ y, const float *__restrict__ g,
              int per_token, SegMap m, int Hk, int H, float scale, float *__restrict__ ws,
              float *__restrict__ total) {
     using Sm = StateSmem<D>;
@@ -190,8 +189,8 @@ state_kernel(const T *__restrict__ x, const T *__restrict__ y, const float *__re
         const int64_t t = sg.t0 + (kReverse ? chunks - 1 - c : c) * kC;
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
         __syncthreads();
-        load_tile<T, D>(sm.x, x, t, L, Hk, h / (H / Hk), D, 0);
-        load_tile<T, W>(sm.y, y, t, L, H, h, D, c0);
+        load_tile<D>(sm.x, x, t, L, Hk, h / (H / Hk), D, 0);
+        load_tile<W>(sm.y, y, t, L, H, h, D, c0);
         chunk_decays(sm.d, g, per_token, t, L, h, H);
         chunk_ready();
         const double tot = sm.d.tot;
@@ -228,11 +227,11 @@ struct OutSmem {
 
 // grid (units, H, D / kW): value columns are independent, so a head is split
 // over blocks of 64 columns (the chunk's 32 x 32 products are formed in each).
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+out_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
            const float *__restrict__ g, int per_token, const float *h0, SegMap m, int Hk, int H,
-           float scale, const float *__restrict__ ws, T *__restrict__ o, float *hT) {
+           float scale, const float *__restrict__ ws, float *__restrict__ o, float *hT) {
     using Sm = OutSmem<D>;
     constexpr int W = Sm::kW;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -254,9 +253,9 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
     for (int64_t t = sg.t0; t < sg.t1; t += kC) {
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
         __syncthreads();
-        load_tile<T, D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
-        load_tile<T, D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
-        load_tile<T, W>(sm.v, v, t, L, H, h, D, c0);
+        load_tile<D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
+        load_tile<D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
+        load_tile<W>(sm.v, v, t, L, H, h, D, c0);
         chunk_decays(sm.d, g, per_token, t, L, h, H);
         chunk_ready();
         Tile<kC, kC> P;
@@ -285,7 +284,7 @@ out_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict
             if (O.m(i) < L)
 #pragma unroll
                 for (int j = 0; j < O.kJ; ++j)
-                    IO<T>::st(o + ((size_t)(t + O.m(i)) * H + h) * D + c0 + O.n(j), O.v[i][j] * scale);
+                    o[((size_t)(t + O.m(i)) * H + h) * D + c0 + O.n(j)] = O.v[i][j] * scale;
         __syncthreads();
         const double tot = sm.d.tot;
         for (int e = threadIdx.x; e < kC * W; e += kThreads)
@@ -324,14 +323,14 @@ struct GradSmem {
 
 // Loads a chunk and forms P = (Q K^T . D) scale and dA = (dO V^T . D) scale in
 // shared memory; kW: P is replaced by W = P . dO V^T.
-template <typename T, int D, bool kW>
-__device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T *k, const T *v,
-                                           const T *dO, const float *g, int per_token, int64_t t,
+template <int D, bool kW>
+__device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const float *q, const float *k, const float *v,
+                                           const float *dO, const float *g, int per_token, int64_t t,
                                            int L, int Hk, int H, int h, float scale) {
-    load_tile<T, D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
-    load_tile<T, D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
-    load_tile<T, D>(sm.v, v, t, L, H, h, D, 0);
-    load_tile<T, D>(sm.dO, dO, t, L, H, h, D, 0);
+    load_tile<D>(sm.q, q, t, L, Hk, h / (H / Hk), D, 0);
+    load_tile<D>(sm.k, k, t, L, Hk, h / (H / Hk), D, 0);
+    load_tile<D>(sm.v, v, t, L, H, h, D, 0);
+    load_tile<D>(sm.dO, dO, t, L, H, h, D, 0);
     chunk_decays(sm.d, g, per_token, t, L, h, H);
     chunk_ready();
     Tile<kC, kC> P, dP;
@@ -351,23 +350,21 @@ __device__ __forceinline__ void grad_chunk(GradSmem<D> &sm, const T *q, const T 
         }
 }
 
-// A gradient row of a head that shares q and k with others goes out in fp32 (to
-// be summed over the group), else rounded.
-template <typename T>
-__device__ __forceinline__ void store_shared(T *out, float *part, size_t e, float x) {
-    if (part != nullptr) part[e] = x;
-    else IO<T>::st(out + e, x);
+// A gradient row of a head that shares q and k with others goes out as a part (to
+// be summed over the group).
+__device__ __forceinline__ void store_shared(float *out, float *part, size_t e, float x) {
+    (part != nullptr ? part : out)[e] = x;
 }
 
 // dQ, the decay term of every row (rowsum W - colsum W + q . dq from the state),
 // and <S_end, E_end> of the segment.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-              const T *__restrict__ dO, const float *__restrict__ g, int per_token,
+grad_q_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+              const float *__restrict__ dO, const float *__restrict__ g, int per_token,
               const float *__restrict__ h0, const float *__restrict__ dhT, SegMap m, int Hk, int H,
               float scale, const float *__restrict__ wsS, const float *__restrict__ wsE,
-              T *__restrict__ dq, float *__restrict__ part, float *__restrict__ term,
+              float *__restrict__ dq, float *__restrict__ part, float *__restrict__ term,
               double *__restrict__ anchor) {
     extern __shared__ __align__(16) unsigned char raw[];
     GradSmem<D> &sm = *reinterpret_cast<GradSmem<D> *>(raw);
@@ -388,7 +385,7 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
     for (int64_t t = sg.t0; t < sg.t1; t += kC) {
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
         __syncthreads();
-        grad_chunk<T, D, true>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
+        grad_chunk<D, true>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
         Tile<kC, D> X;                                 // dO S^T
         X.zero();
         X.template mac<D, false, true>(sm.dO, D + kPad, sm.S, D + kPad);
@@ -456,14 +453,14 @@ grad_q_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restr
 }
 
 // dK, dV, dg and dh0, chunks last to first.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-               const T *__restrict__ dO, const float *__restrict__ g, int per_token,
+grad_kv_kernel(const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
+               const float *__restrict__ dO, const float *__restrict__ g, int per_token,
                const float *__restrict__ dhT, SegMap m, int Hk, int H, float scale,
                const float *__restrict__ wsE, const float *__restrict__ term,
-               const double *__restrict__ anchor, T *__restrict__ dk, float *__restrict__ part,
-               T *__restrict__ dv, float *__restrict__ dg, double *__restrict__ head_sum,
+               const double *__restrict__ anchor, float *__restrict__ dk, float *__restrict__ part,
+               float *__restrict__ dv, float *__restrict__ dg, double *__restrict__ head_sum,
                float *__restrict__ dh0) {
     extern __shared__ __align__(16) unsigned char raw[];
     GradSmem<D> &sm = *reinterpret_cast<GradSmem<D> *>(raw);
@@ -489,7 +486,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
         const int64_t t = sg.t0 + c * kC;
         const int L = (int)(sg.t1 - t < kC ? sg.t1 - t : kC);
         __syncthreads();
-        grad_chunk<T, D, false>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
+        grad_chunk<D, false>(sm, q, k, v, dO, g, per_token, t, L, Hk, H, h, scale);
         const double tot = sm.d.tot;
         Tile<kC, D> X;                                 // V E^T
         X.zero();
@@ -531,7 +528,7 @@ grad_kv_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
             if (X.m(i) < L)
 #pragma unroll
                 for (int j = 0; j < X.kJ; ++j)
-                    IO<T>::st(dv + ((size_t)(t + X.m(i)) * H + h) * D + X.n(j), X.v[i][j]);
+                    dv[((size_t)(t + X.m(i)) * H + h) * D + X.n(j)] = X.v[i][j];
         __syncthreads();
         for (int e = threadIdx.x; e < kC * D; e += kThreads)
             sm.dO[e / D * (D + kPad) + e % D] *= scale * sm.d.row[e / D];
