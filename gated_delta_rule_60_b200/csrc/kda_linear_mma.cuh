@@ -5,16 +5,18 @@
 // Why warp-level.  The gradient of the decays is a small difference of large sums
 // and goes out in fp32, so its products with the state need the state to 24 bits:
 // three bf16 terms.  Here the state is a register accumulator whose fragments are
-// the next product's left operand as they are, and are cut into terms in registers;
-// for tcgen05 each term is a tile to be written to tensor memory or shared memory
-// per chunk, which does not leave room for two stages of four input tiles.
+// the next product's left operand as they are, and are cut into terms in registers.
+// On tcgen05 each term would be written to tensor memory for every chunk, as the
+// prefill writes those of V' (192 columns of 512 at d = 128): another kernel, which
+// is not built.  Rounded to bf16 once each, on top of the outputs' own rounding: P, dA,
+// the state that the queries of a prefill read, and E where dV reads it.
 //
 // The state X (D x D, fp32) is spread over NW = D / 16 warps, 16 rows each.  With
 // 64-token chunks, tiles of tokens in shared memory (rows padded by 16 bytes: every
 // ldmatrix is free of bank conflicts), filled by asynchronous copies a chunk ahead:
 //   X (+)= (Diag(c) A)^T B     A^T by transposing loads, scaled and cut in registers
 //   Y^T = X B^T                X's accumulators as the left operand
-// What bounds it: at d = 128 a block has 8 warps of 255 registers (two a scheduler),
+// What bounds the gradient: at d = 128 a block has 8 warps of 255 registers (two a scheduler),
 // and the tensor pipe is busy for 40 to 43 % of the time; the rest waits for
 // shared memory and for one matrix instruction after another.  96 heads x 2,048
 // tokens: dQ 194 us, dK and dV 240 us.

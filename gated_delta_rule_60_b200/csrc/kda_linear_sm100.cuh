@@ -44,13 +44,15 @@
 // Shared memory: two stages of Q, K, V (96 KB each; O leaves through Q's tile) and
 // S'' (32 KB).
 //
-// Measured: 96 heads x 8,192 tokens 249 us (3.3 TB/s; 125 us of it are the bytes at
+// Measured: 96 heads x 8,192 tokens 246 us (3.3 TB/s; 125 us of it are the bytes at
 // the rate of a copy), 87,469 packed tokens of 32 heads 577 us behind 11 us of states
 // and scan, 16 heads x 131,072 tokens 430 us behind 235 us of states.  Neither memory
 // nor the tensor cores bound it (half and a quarter busy): a chunk takes 6 to 7
-// thousand cycles of dependent steps, S to S'' to O and V' to S, and tensor memory is
-// full, so that no second chunk fits beside the first.  Two terms of V' instead of
-// three would make room, and leave the final state with an error of 2.7e-6.
+// thousand cycles of dependent steps, S to S'' to O and V' to S, and in this division
+// of tensor memory Q K^T of the next chunk waits until O has been read.  An O with
+// columns of its own (P' over what Q K^T leaves, V' in quarters) is not built; two
+// terms of V' instead of three would make the room too, and leave the final state with
+// an error of 2.7e-6.
 #pragma once
 
 #include "kda_linear_common.cuh"
@@ -153,8 +155,8 @@ __device__ __forceinline__ void tmem_st_frag(uint32_t addr, const uint32_t (&r)[
                  : "memory");
 }
 
-// level ln 2, in two parts: the first has 10 bits, and what its product with a
-// large level does not hold is kept too.
+// level ln 2, with ln 2 split in two parts (Cody and Waite): the first has 10 bits,
+// and what its product with a large level does not hold is kept too.
 __device__ __forceinline__ Sum2 level_sum(int level) {
     const float l = (float)level, hi = l * 0.693359375f;
     return add2({hi, fmaf(l, 0.693359375f, -hi)}, {l * -2.12194440054690583e-4f, 0.f});
